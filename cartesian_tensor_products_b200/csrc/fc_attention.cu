@@ -1,0 +1,326 @@
+// Node attention, forward.
+//
+// One block takes 64 virtual rows (receivers x heads of a key head) of one
+// structure and walks over its senders with a running maximum and sum: scores,
+// cap, distance bias and mask stay in registers, keys and values pass through
+// a double-buffered shared tile.  With few rows the senders are split over
+// blocks whose partial rows a second kernel joins.
+#include <math.h>
+
+#include "fc_attention.cuh"
+
+namespace fc {
+
+template <class T, int DP>
+struct FwdSmem {
+  static constexpr int BN = kStep<T, DP>, S = kStride<T, DP>;
+  static constexpr size_t kv = sizeof(T) * BN * S;
+  static constexpr size_t q = sizeof(T) * 64 * S;
+  static constexpr size_t bytes = q + 4 * kv + 2 * BN * sizeof(float4);
+};
+
+template <class T, int DP, bool Two>
+__global__ void __launch_bounds__(128) attn_fwd_kernel(AttnArgs a) {
+  constexpr int BN = kStep<T, DP>, NT = BN / 8, S = kStride<T, DP>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  T* qs = reinterpret_cast<T*>(smem);
+  T* ks = qs + 64 * S;             // two stages
+  T* vs = ks + 2 * BN * S;
+  float4* info = reinterpret_cast<float4*>(vs + 2 * BN * S);   // [2][BN]: sender position, w = 1 if not there
+  TileAt at;
+  if (!find_tile(a.recv_ptr, a.B, a.nr, a.G, 64, blockIdx.x, at)) return;
+  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int slo, shi;
+  other_side(a.send_ptr, a.B, a.ns, at.b, slo, shi);
+  const int all = shi > slo ? (shi - slo + BN - 1) / BN : 0;
+  const int t0 = (int)((long long)all * blockIdx.z / a.splits), t1 = (int)((long long)all * (blockIdx.z + 1) / a.splits);
+
+  const T* q = static_cast<const T*>(a.q);
+  const T* k = static_cast<const T*>(a.k) + (long long)kvh * a.D;
+  const T* v = static_cast<const T*>(a.v) + (long long)kvh * a.D;
+  auto qrow = [&](int r) {
+    const long long vr = at.v0 + r < at.v1 ? at.v0 + r : at.v0;
+    return q + vr / a.G * a.ldq + (kvh * a.G + vr % a.G) * (long long)a.D;
+  };
+  load_rows<T, DP, 64, 128>(qs, a.D, tid, qrow, [&](int r) { return at.v0 + r < at.v1; });
+  auto load_kv = [&](int t, int st) {
+    const long long j0 = slo + (long long)t * BN;
+    auto live = [&](int r) { return j0 + r < shi && (!a.mask || a.mask[j0 + r]); };
+    load_rows<T, DP, BN, 128>(ks + st * BN * S, a.D, tid, [&](int r) { return k + (j0 + r) * a.ldk; }, live);
+    load_rows<T, DP, BN, 128>(vs + st * BN * S, a.D, tid, [&](int r) { return v + (j0 + r) * a.ldv; }, live);
+    if (tid < BN) {
+      float4 f = make_float4(0.f, 0.f, 0.f, live(tid) ? 0.f : 1.f);
+      if (a.pos_r && live(tid)) {
+        const float* p = a.pos_s + 3 * (j0 + tid);
+        f.x = p[0]; f.y = p[1]; f.z = p[2];
+      }
+      info[st * BN + tid] = f;
+    }
+  };
+  if (t0 < t1) load_kv(t0, 0);
+  cp_commit();
+
+  // the two rows of this thread
+  const int g = lane >> 2, c2 = 2 * (lane & 3);
+  long long vr[2];
+  float px[2], py[2], pz[2], sl[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    vr[h] = at.v0 + warp * 16 + g + 8 * h;
+    const long long r = vr[h] < at.v1 ? vr[h] : at.v0;
+    px[h] = py[h] = pz[h] = sl[h] = 0.0f;
+    if (a.pos_r) {
+      const float* p = a.pos_r + 3 * (r / a.G);
+      px[h] = p[0]; py[h] = p[1]; pz[h] = p[2];
+      sl[h] = a.slope[kvh * a.G + r % a.G] * kLog2e;
+    }
+  }
+  const float mul = a.cap > 0.0f ? a.scale / a.cap : a.scale * kLog2e;
+  const float cap2 = a.cap * kLog2e;
+  float acc[DP / 8][4];
+#pragma unroll
+  for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[d][e] = 0.0f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+  for (int t = t0; t < t1; ++t) {
+    const int st = (t - t0) & 1;
+    if (t + 1 < t1) load_kv(t + 1, st ^ 1);
+    cp_commit();
+    cp_wait<1>();
+    __syncthreads();
+    const float4* in = info + st * BN;
+    float s[NT][4];
+    strip_nt<T, DP, NT>(s, qs + warp * 16 * S, ks + st * BN * S);
+    if (a.cap > 0.0f) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = cap2 * cap_tanh<T>(s[n][e] * mul);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] *= mul;
+    }
+    if (a.pos_r) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float4 f = in[n * 8 + c2 + c];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float dx = px[h] - f.x, dy = py[h] - f.y, dz = pz[h] - f.z;
+            const float d2 = dx * dx + dy * dy + dz * dz;
+            s[n][2 * h + c] -= sl[h] * (d2 > 0.0f ? d2 * rsq(d2) : 0.0f);
+          }
+        }
+    }
+    const bool ragged = a.mask || slo + (long long)(t + 1) * BN > shi;
+    if (ragged) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (in[n * 8 + c2 + c].w != 0.0f) s[n][c] = s[n][2 + c] = -INFINITY;
+    }
+    float alpha[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mx = m[h];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * h], s[n][2 * h + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float base = mx == -INFINITY ? 0.0f : mx;
+      alpha[h] = ex2(m[h] - base);
+      m[h] = mx;
+      float sum = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float p = ex2(s[n][2 * h + c] - base);
+          s[n][2 * h + c] = p;
+          sum += p;
+        }
+      l[h] = l[h] * alpha[h] + sum;
+    }
+    strip_pn<T, DP, NT, Two>(acc, s, vs + st * BN * S, alpha[0], alpha[1]);
+    __syncthreads();
+  }
+  cp_wait<0>();
+
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float sum = l[h];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if (vr[h] >= at.v1) continue;
+    const long long node = vr[h] / a.G;
+    const int head = kvh * a.G + (int)(vr[h] % a.G);
+    const long long row = node * a.H + head;
+    if (a.splits > 1) {
+      const long long pr = (long long)blockIdx.z * a.nr * a.H + row;
+      if ((lane & 3) == 0) a.part_ml[pr] = make_float2(m[h], sum);
+#pragma unroll
+      for (int d = 0; d < DP / 8; ++d)
+        if (d * 8 < a.D)
+          *reinterpret_cast<float2*>(a.part + pr * a.D + d * 8 + c2) = make_float2(acc[d][2 * h], acc[d][2 * h + 1]);
+      continue;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (a.lse && (lane & 3) == 0) a.lse[row] = (m[h] + log2f(sum)) * kLn2;
+    T* o = static_cast<T*>(a.out) + node * a.ldo + (long long)head * a.D;
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) {
+      if (d * 8 >= a.D) continue;
+      const float v2[2] = {acc[d][2 * h] * inv, acc[d][2 * h + 1] * inv};
+      store_pack<T, 2>(o + d * 8 + c2, v2);
+      if (a.o32) store_pack<float, 2>(a.o32 + row * a.D + d * 8 + c2, v2);
+    }
+  }
+}
+
+// Joins the parts of a row: the largest maximum, the parts rescaled to it.
+// One warp per row and head.
+template <class T>
+__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a) {
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long node = row / a.H;
+  const int head = (int)(row - node * a.H);
+  if (node >= a.nr) return;
+  const long long step = (long long)a.nr * a.H;
+  float m = -INFINITY;
+  for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.part_ml[s * step + row].x);
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == -INFINITY ? 0.0f : m;
+  float sum = 0.0f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const int c = lane * 4;
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 ml = a.part_ml[s * step + row];
+    const float w = ex2(ml.x - base);
+    sum += w * ml.y;
+    if (c < a.D) {
+      const float4 v = *reinterpret_cast<const float4*>(a.part + (s * step + row) * a.D + c);
+      acc[0] += w * v.x; acc[1] += w * v.y; acc[2] += w * v.z; acc[3] += w * v.w;
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (a.lse && lane == 0) a.lse[row] = (m + log2f(sum)) * kLn2;
+  if (c < a.D) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] *= inv;
+    store_pack<T, 4>(static_cast<T*>(a.out) + node * a.ldo + (long long)head * a.D + c, acc);
+    if (a.o32) store_pack<float, 4>(a.o32 + row * a.D + c, acc);
+  }
+}
+
+// ----------------------------------------------------------------- launches
+
+int check_attn(const fc_attn_desc* d, int n_struct, int n_recv, int n_send) {
+  if (!d || !row_dtype(d->dtype) || n_struct < 0 || n_recv < 0 || n_send < 0) return FC_ERR_ARG;
+  if (d->heads < 1 || d->kv_heads < 1 || d->heads > 1024 || d->kv_heads > d->heads || d->heads % d->kv_heads)
+    return FC_ERR_ARG;
+  if (d->head_dim < 8 || d->head_dim > 128) return FC_ERR_ARG;
+  if (!isfinite(d->scale) || !isfinite(d->cap) || d->cap < 0.0f) return FC_ERR_ARG;
+  if (d->head_dim % 8) return FC_ERR_ALIGN;
+  return FC_OK;
+}
+
+int attn_pad(int head_dim) { return head_dim <= 32 ? 32 : head_dim <= 64 ? 64 : 128; }
+
+// Parts of the key range: enough blocks for two per SM, each part at least
+// four product steps of an average structure.
+int attn_splits(int B, int nr, int ns, int G, int KV, int step) {
+  const long long blocks = ((long long)nr * G + 63) / 64 * KV;
+  const long long per = B > 0 ? ns / B : 0;
+  const long long want = blocks > 0 ? 2LL * device_sm_count() / blocks : 1;
+  const long long most = per / (4 * step);
+  long long s = want < most ? want : most;
+  if (s > 64) s = 64;
+  return s < 1 ? 1 : (int)s;
+}
+
+static int fwd_step(const fc_attn_desc* d) { return d->dtype == FC_F32 && d->head_dim > 64 ? 32 : 64; }
+
+template <class T, int DP, bool Two>
+static int run_attn(const AttnArgs& a, cudaStream_t s) {
+  static DeviceFlags ready;
+  constexpr size_t bytes = FwdSmem<T, DP>::bytes;
+  if (set_smem_once(ready, attn_fwd_kernel<T, DP, Two>, bytes) != FC_OK) return FC_ERR_CUDA;
+  attn_fwd_kernel<T, DP, Two><<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, 64), a.KV, a.splits), 128, bytes, s>>>(a);
+  if (a.splits > 1)
+    attn_join_kernel<T><<<(unsigned)(((long long)a.nr * a.H + 7) / 8), 256, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
+}
+
+template <class T>
+static int run_attn_type(const AttnArgs& a, cudaStream_t s) {
+  const bool two = sizeof(T) == 2 && a.o32;
+  switch (attn_pad(a.D)) {
+    case 32: return two ? run_attn<T, 32, sizeof(T) == 2>(a, s) : run_attn<T, 32, false>(a, s);
+    case 64: return two ? run_attn<T, 64, sizeof(T) == 2>(a, s) : run_attn<T, 64, false>(a, s);
+    default: return two ? run_attn<T, 128, sizeof(T) == 2>(a, s) : run_attn<T, 128, false>(a, s);
+  }
+}
+
+}  // namespace fc
+
+using namespace fc;
+
+extern "C" {
+
+size_t fc_node_attention_workspace_size(const fc_attn_desc* desc, int n_struct, int n_recv, int n_send) {
+  if (check_attn(desc, n_struct, n_recv, n_send) != FC_OK || n_recv == 0) return 0;
+  const int sp = attn_splits(n_struct, n_recv, n_send, desc->heads / desc->kv_heads, desc->kv_heads, fwd_step(desc));
+  if (sp == 1) return 0;
+  const size_t rows = (size_t)sp * n_recv * desc->heads;
+  return round16(rows * desc->head_dim * sizeof(float)) + round16(rows * sizeof(float2));
+}
+
+int fc_node_attention(const fc_attn_desc* desc, int n_struct, int n_recv, int n_send, const int32_t* recv_ptr,
+                      const int32_t* send_ptr, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                      int64_t ldv, const float* pos_recv, const float* pos_send, const float* slope,
+                      const uint8_t* send_mask, void* out, int64_t ldo, float* lse, float* out_f32, void* workspace,
+                      size_t ws_bytes, fc_stream_t stream) {
+  const int st = check_attn(desc, n_struct, n_recv, n_send);
+  if (st != FC_OK) return st;
+  if (n_recv == 0) return FC_OK;
+  const int D = desc->head_dim, H = desc->heads, KV = desc->kv_heads;
+  if (!recv_ptr || !send_ptr || !q || !out || (n_send > 0 && (!k || !v))) return FC_ERR_ARG;
+  if (!pos_recv != !slope || (pos_send && !pos_recv)) return FC_ERR_ARG;
+  if (pos_recv && !pos_send && n_recv != n_send) return FC_ERR_ARG;
+  if (ldq < (int64_t)H * D || ldo < (int64_t)H * D || (n_send > 0 && (ldk < (int64_t)KV * D || ldv < (int64_t)KV * D)))
+    return FC_ERR_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(k) || !aligned16(v) || !aligned16(out_f32) || ldq % 8 || ldk % 8 ||
+      ldv % 8 || ldo % 8 || !aligned4(recv_ptr) || !aligned4(send_ptr) || !aligned4(pos_recv) || !aligned4(pos_send) ||
+      !aligned4(slope) || !aligned4(lse))
+    return FC_ERR_ALIGN;
+  AttnArgs a{};
+  a.B = n_struct; a.nr = n_recv; a.ns = n_send; a.H = H; a.KV = KV; a.G = H / KV; a.D = D;
+  a.scale = desc->scale; a.cap = desc->cap;
+  a.ldq = ldq; a.ldk = ldk; a.ldv = ldv; a.ldo = ldo;
+  a.recv_ptr = recv_ptr; a.send_ptr = send_ptr; a.q = q; a.k = k; a.v = v;
+  a.pos_r = pos_recv; a.pos_s = pos_send ? pos_send : pos_recv; a.slope = slope; a.mask = send_mask;
+  a.out = out; a.lse = lse; a.o32 = out_f32;
+  a.splits = attn_splits(n_struct, n_recv, n_send, a.G, KV, fwd_step(desc));
+  if (tile_slots(a.B, a.nr, a.G, 64) > INT32_MAX) return FC_ERR_ARG;
+  if (a.splits > 1) {
+    const size_t need = fc_node_attention_workspace_size(desc, n_struct, n_recv, n_send);
+    if (!workspace || ws_bytes < need) return FC_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return FC_ERR_ALIGN;
+    a.part = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) +
+                                          round16((size_t)a.splits * n_recv * H * D * sizeof(float)));
+  }
+  cudaStream_t s = (cudaStream_t)stream;
+  if (desc->dtype == FC_F32) return run_attn_type<float>(a, s);
+  if (desc->dtype == FC_BF16) return run_attn_type<__nv_bfloat16>(a, s);
+  return run_attn_type<__half>(a, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,530 @@
+// Node attention, gradient.
+//
+// Two passes over the score matrix, both recomputing the weights from the
+// saved log-sums, so that every gradient is a sum held by one block and no
+// atomics are needed: one block per 64 virtual rows for the query gradient
+// (with the receiver and slope sums), one per 64 senders and key head for the
+// key and value gradients (with the sender position sums; the heads of the
+// group are virtual rows and sum by themselves).  A small kernel first forms
+// delta = g . out from the FP32 output, and small ones at the end add the
+// position and slope sums over heads and nodes.
+#include <math.h>
+
+#include "fc_attention.cuh"
+
+namespace fc {
+
+// [nr H]: log-sum in base 2 (+inf for rows without senders, whose weights are
+// then 0) and delta.  Eight lanes per row and head.
+template <class T>
+__global__ void __launch_bounds__(256) attn_stat_kernel(AttnArgs a, const float* __restrict__ o32,
+                                                        const float* __restrict__ lse, float2* __restrict__ stat) {
+  const long long row = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);
+  const int lane = threadIdx.x & 7;
+  const bool live = row < (long long)a.nr * a.H;
+  const long long node = live ? row / a.H : 0;
+  const T* g = static_cast<const T*>(a.g) + node * a.ldg + (live ? row - node * a.H : 0) * a.D;
+  float d = 0.0f;
+  if (live)
+    for (int c = lane * 4; c < a.D; c += 32) {
+      float x[4], y[4];
+      load_pack<T, 4>(g + c, x);
+      load_pack<float, 4>(o32 + row * a.D + c, y);
+      d += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
+    }
+  for (int o = 4; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  if (live && lane == 0) {
+    const float l = lse[row];
+    stat[row] = make_float2(l == -INFINITY ? INFINITY : l * kLog2e, d);
+  }
+}
+
+// Score in base 2 and the derivative of the cap, from the raw product.
+template <class T>
+__device__ __forceinline__ void capped(const AttnArgs& a, float raw, float mul, float cap2, float& t, float& dc) {
+  if (a.cap > 0.0f) {
+    const float th = cap_tanh<T>(raw * mul);
+    t = cap2 * th;
+    dc = 1.0f - th * th;
+  } else {
+    t = raw * mul;
+    dc = 1.0f;
+  }
+}
+
+template <class T, int DP>
+struct VjpSmem {
+  static constexpr int BN = kStep<T, DP> == 64 && DP > 64 ? 32 : kStep<T, DP>;   // streamed rows
+  static constexpr int S = kStride<T, DP>;
+  static constexpr size_t bytes = sizeof(T) * 64 * S * 2 + sizeof(T) * BN * S * 4 + 4 * BN * sizeof(float4);
+};
+
+// Query gradient, receiver position sums and slope sums.
+template <class T, int DP>
+__global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
+  constexpr int BN = VjpSmem<T, DP>::BN, NT = BN / 8, S = kStride<T, DP>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  T* qs = reinterpret_cast<T*>(smem);
+  T* gs = qs + 64 * S;
+  T* ks = gs + 64 * S;
+  T* vs = ks + 2 * BN * S;
+  float4* info = reinterpret_cast<float4*>(vs + 2 * BN * S);
+  TileAt at;
+  if (!find_tile(a.recv_ptr, a.B, a.nr, a.G, 64, blockIdx.x, at)) return;
+  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int slo, shi;
+  other_side(a.send_ptr, a.B, a.ns, at.b, slo, shi);
+  const int all = shi > slo ? (shi - slo + BN - 1) / BN : 0;
+  const int t0 = (int)((long long)all * blockIdx.z / a.splits), t1 = (int)((long long)all * (blockIdx.z + 1) / a.splits);
+  const T* k = static_cast<const T*>(a.k) + (long long)kvh * a.D;
+  const T* v = static_cast<const T*>(a.v) + (long long)kvh * a.D;
+  auto rowat = [&](const T* base, long long ld, int r) {
+    const long long vr = at.v0 + r < at.v1 ? at.v0 + r : at.v0;
+    return base + vr / a.G * ld + (kvh * a.G + vr % a.G) * (long long)a.D;
+  };
+  auto inside = [&](int r) { return at.v0 + r < at.v1; };
+  load_rows<T, DP, 64, 128>(qs, a.D, tid, [&](int r) { return rowat(static_cast<const T*>(a.q), a.ldq, r); }, inside);
+  load_rows<T, DP, 64, 128>(gs, a.D, tid, [&](int r) { return rowat(static_cast<const T*>(a.g), a.ldg, r); }, inside);
+  auto load_kv = [&](int t, int st) {
+    const long long j0 = slo + (long long)t * BN;
+    auto live = [&](int r) { return j0 + r < shi && (!a.mask || a.mask[j0 + r]); };
+    load_rows<T, DP, BN, 128>(ks + st * BN * S, a.D, tid, [&](int r) { return k + (j0 + r) * a.ldk; }, live);
+    load_rows<T, DP, BN, 128>(vs + st * BN * S, a.D, tid, [&](int r) { return v + (j0 + r) * a.ldv; }, live);
+    if (tid < BN) {
+      float4 f = make_float4(0.f, 0.f, 0.f, live(tid) ? 0.f : 1.f);
+      if (a.pos_r && live(tid)) {
+        const float* p = a.pos_s + 3 * (j0 + tid);
+        f.x = p[0]; f.y = p[1]; f.z = p[2];
+      }
+      info[st * BN + tid] = f;
+    }
+  };
+  if (t0 < t1) load_kv(t0, 0);
+  cp_commit();
+
+  const int g = lane >> 2, c2 = 2 * (lane & 3);
+  long long vr[2];
+  float px[2], py[2], pz[2], sl[2], lse2[2], delta[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    vr[h] = at.v0 + warp * 16 + g + 8 * h;
+    const long long r = vr[h] < at.v1 ? vr[h] : at.v0;
+    const int head = kvh * a.G + (int)(r % a.G);
+    px[h] = py[h] = pz[h] = sl[h] = 0.0f;
+    if (a.pos_r) {
+      const float* p = a.pos_r + 3 * (r / a.G);
+      px[h] = p[0]; py[h] = p[1]; pz[h] = p[2];
+      sl[h] = a.slope[head];
+    }
+    const float2 st = a.stat[r / a.G * a.H + head];
+    lse2[h] = vr[h] < at.v1 ? st.x : INFINITY;
+    delta[h] = st.y;
+  }
+  const float mul = a.cap > 0.0f ? a.scale / a.cap : a.scale * kLog2e;
+  const float cap2 = a.cap * kLog2e;
+  float acc[DP / 8][4], bx[2] = {0.f, 0.f}, by[2] = {0.f, 0.f}, bz[2] = {0.f, 0.f}, bs[2] = {0.f, 0.f};
+#pragma unroll
+  for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[d][e] = 0.0f;
+
+  for (int t = t0; t < t1; ++t) {
+    const int st = (t - t0) & 1;
+    if (t + 1 < t1) load_kv(t + 1, st ^ 1);
+    cp_commit();
+    cp_wait<1>();
+    __syncthreads();
+    const float4* in = info + st * BN;
+    float s[NT][4], dp[NT][4];
+    strip_nt<T, DP, NT>(s, qs + warp * 16 * S, ks + st * BN * S);
+    strip_nt<T, DP, NT>(dp, gs + warp * 16 * S, vs + st * BN * S);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float4 f = in[n * 8 + c2 + c];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float tt, dc;
+          capped<T>(a, s[n][2 * h + c], mul, cap2, tt, dc);
+          float dx = 0.f, dy = 0.f, dz = 0.f, inv = 0.f, dist = 0.f;
+          if (a.pos_r) {
+            dx = px[h] - f.x; dy = py[h] - f.y; dz = pz[h] - f.z;
+            const float d2 = dx * dx + dy * dy + dz * dz;
+            inv = d2 > 0.0f ? rsq(d2) : 0.0f;
+            dist = d2 * inv;
+            tt -= sl[h] * kLog2e * dist;
+          }
+          const float p = ex2(tt - lse2[h]);
+          const float dt = f.w != 0.0f ? 0.0f : p * (dp[n][2 * h + c] - delta[h]);
+          if (a.pos_r) {
+            const float w = dt * inv;
+            bx[h] += w * dx; by[h] += w * dy; bz[h] += w * dz;
+            bs[h] += dt * dist;
+          }
+          s[n][2 * h + c] = dt * dc;
+        }
+      }
+    strip_pn<T, DP, NT, false>(acc, s, ks + st * BN * S, 1.0f, 1.0f);
+    __syncthreads();
+  }
+  cp_wait<0>();
+
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      bx[h] += __shfl_xor_sync(0xffffffffu, bx[h], o);
+      by[h] += __shfl_xor_sync(0xffffffffu, by[h], o);
+      bz[h] += __shfl_xor_sync(0xffffffffu, bz[h], o);
+      bs[h] += __shfl_xor_sync(0xffffffffu, bs[h], o);
+    }
+    if (vr[h] >= at.v1) continue;
+    const long long row = vr[h] / a.G * a.H + kvh * a.G + (int)(vr[h] % a.G);
+    const long long pr = (long long)blockIdx.z * a.nr * a.H + row;
+    if (a.rowpart && (lane & 3) == 0)
+      a.rowpart[pr] = make_float4(-sl[h] * bx[h], -sl[h] * by[h], -sl[h] * bz[h], -bs[h]);
+    if (!a.qb) continue;
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) {
+      if (d * 8 >= a.D) continue;
+      const float v2[2] = {acc[d][2 * h] * a.scale, acc[d][2 * h + 1] * a.scale};
+      if (a.splits > 1)
+        store_pack<float, 2>(a.part + pr * a.D + d * 8 + c2, v2);
+      else
+        store_pack<T, 2>(static_cast<T*>(a.qb) + row * a.D + d * 8 + c2, v2);
+    }
+  }
+}
+
+// Key and value gradients and sender position sums.
+template <class T, int DP>
+__global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
+  constexpr int BN = VjpSmem<T, DP>::BN, NT = BN / 8, S = kStride<T, DP>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  T* ks = reinterpret_cast<T*>(smem);
+  T* vs = ks + 64 * S;
+  T* qs = vs + 64 * S;
+  T* gs = qs + 2 * BN * S;
+  float4* rpos = reinterpret_cast<float4*>(gs + 2 * BN * S);   // [2][BN]: receiver position, slope
+  float4* rst = rpos + 2 * BN;                                 // [2][BN]: log-sum, delta
+  TileAt at;
+  if (!find_tile(a.send_ptr, a.B, a.ns, 1, 64, blockIdx.x, at)) return;
+  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int rlo, rhi;
+  other_side(a.recv_ptr, a.B, a.nr, at.b, rlo, rhi);
+  const long long r0 = (long long)rlo * a.G, r1 = (long long)rhi * a.G;
+  const long long steps = r1 > r0 ? (r1 - r0 + BN - 1) / BN : 0;
+  auto shown = [&](long long j) { return j < at.v1 && (!a.mask || a.mask[j]); };
+  auto live = [&](int r) { return shown(at.v0 + r); };
+  load_rows<T, DP, 64, 128>(
+      ks, a.D, tid, [&](int r) { return static_cast<const T*>(a.k) + (at.v0 + r) * a.ldk + (long long)kvh * a.D; }, live);
+  load_rows<T, DP, 64, 128>(
+      vs, a.D, tid, [&](int r) { return static_cast<const T*>(a.v) + (at.v0 + r) * a.ldv + (long long)kvh * a.D; }, live);
+  auto load_q = [&](long long t, int st) {
+    const long long b = r0 + t * BN;
+    auto at_row = [&](const T* base, long long ld, int r) {
+      return base + (b + r) / a.G * ld + (kvh * a.G + (b + r) % a.G) * (long long)a.D;
+    };
+    auto in = [&](int r) { return b + r < r1; };
+    load_rows<T, DP, BN, 128>(qs + st * BN * S, a.D, tid,
+                              [&](int r) { return at_row(static_cast<const T*>(a.q), a.ldq, r); }, in);
+    load_rows<T, DP, BN, 128>(gs + st * BN * S, a.D, tid,
+                              [&](int r) { return at_row(static_cast<const T*>(a.g), a.ldg, r); }, in);
+    if (tid < BN) {
+      float4 p = make_float4(0.f, 0.f, 0.f, 0.f), s = make_float4(INFINITY, 0.f, 0.f, 0.f);
+      if (b + tid < r1) {
+        const long long node = (b + tid) / a.G;
+        const int head = kvh * a.G + (int)((b + tid) % a.G);
+        if (a.pos_r) p = make_float4(a.pos_r[3 * node], a.pos_r[3 * node + 1], a.pos_r[3 * node + 2], a.slope[head]);
+        const float2 ld = a.stat[node * a.H + head];
+        s.x = ld.x;
+        s.y = ld.y;
+      }
+      rpos[st * BN + tid] = p;
+      rst[st * BN + tid] = s;
+    }
+  };
+  if (steps > 0) load_q(0, 0);
+  cp_commit();
+
+  const int g = lane >> 2, c2 = 2 * (lane & 3);
+  long long vj[2];
+  float px[2], py[2], pz[2];
+  bool keep[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    vj[h] = at.v0 + warp * 16 + g + 8 * h;
+    keep[h] = shown(vj[h]);
+    px[h] = py[h] = pz[h] = 0.0f;
+    if (a.pos_r && keep[h]) {
+      const float* p = a.pos_s + 3 * vj[h];
+      px[h] = p[0]; py[h] = p[1]; pz[h] = p[2];
+    }
+  }
+  const float mul = a.cap > 0.0f ? a.scale / a.cap : a.scale * kLog2e;
+  const float cap2 = a.cap * kLog2e;
+  float dk[DP / 8][4], dv[DP / 8][4], bx[2] = {0.f, 0.f}, by[2] = {0.f, 0.f}, bz[2] = {0.f, 0.f};
+#pragma unroll
+  for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dk[d][e] = dv[d][e] = 0.0f;
+
+  for (long long t = 0; t < steps; ++t) {
+    const int st = (int)(t & 1);
+    if (t + 1 < steps) load_q(t + 1, st ^ 1);
+    cp_commit();
+    cp_wait<1>();
+    __syncthreads();
+    const float4 *rp = rpos + st * BN, *rs = rst + st * BN;
+    float s[NT][4], dp[NT][4];
+    strip_nt<T, DP, NT>(s, ks + warp * 16 * S, qs + st * BN * S);
+    strip_nt<T, DP, NT>(dp, vs + warp * 16 * S, gs + st * BN * S);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float4 f = rp[n * 8 + c2 + c];
+        const float2 ld = *reinterpret_cast<const float2*>(&rs[n * 8 + c2 + c]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float tt, dc;
+          capped<T>(a, s[n][2 * h + c], mul, cap2, tt, dc);
+          float dx = 0.f, dy = 0.f, dz = 0.f, inv = 0.f;
+          if (a.pos_r) {
+            dx = f.x - px[h]; dy = f.y - py[h]; dz = f.z - pz[h];
+            const float d2 = dx * dx + dy * dy + dz * dz;
+            inv = d2 > 0.0f ? rsq(d2) : 0.0f;
+            tt -= f.w * kLog2e * (d2 * inv);
+          }
+          const float p = keep[h] ? ex2(tt - ld.x) : 0.0f;
+          const float dt = keep[h] ? p * (dp[n][2 * h + c] - ld.y) : 0.0f;
+          if (a.pos_r) {
+            const float w = dt * f.w * inv;
+            bx[h] += w * dx; by[h] += w * dy; bz[h] += w * dz;
+          }
+          s[n][2 * h + c] = p;
+          dp[n][2 * h + c] = dt * dc;
+        }
+      }
+    strip_pn<T, DP, NT, false>(dv, s, gs + st * BN * S, 1.0f, 1.0f);
+    strip_pn<T, DP, NT, false>(dk, dp, qs + st * BN * S, 1.0f, 1.0f);
+    __syncthreads();
+  }
+  cp_wait<0>();
+
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      bx[h] += __shfl_xor_sync(0xffffffffu, bx[h], o);
+      by[h] += __shfl_xor_sync(0xffffffffu, by[h], o);
+      bz[h] += __shfl_xor_sync(0xffffffffu, bz[h], o);
+    }
+    if (vj[h] >= at.v1) continue;
+    if (a.colpart && (lane & 3) == 0)
+      a.colpart[(long long)kvh * a.ns + vj[h]] =
+          keep[h] ? make_float4(bx[h], by[h], bz[h], 0.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const long long row = vj[h] * a.KV + kvh;
+    // a hidden sender's row is 0 even where the receivers hold NaN
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) {
+      if (d * 8 >= a.D) continue;
+      const float k2[2] = {keep[h] ? dk[d][2 * h] * a.scale : 0.0f, keep[h] ? dk[d][2 * h + 1] * a.scale : 0.0f};
+      const float v2[2] = {keep[h] ? dv[d][2 * h] : 0.0f, keep[h] ? dv[d][2 * h + 1] : 0.0f};
+      if (a.kb) store_pack<T, 2>(static_cast<T*>(a.kb) + row * a.D + d * 8 + c2, k2);
+      if (a.vb) store_pack<T, 2>(static_cast<T*>(a.vb) + row * a.D + d * 8 + c2, v2);
+    }
+  }
+}
+
+// Adds the parts of the query gradient.  One warp per row and head.
+template <class T>
+__global__ void __launch_bounds__(256) attn_vjp_join_kernel(AttnArgs a) {
+  const int c = (threadIdx.x & 31) * 4;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long node = row / a.H;
+  if (node >= a.nr || c >= a.D) return;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < a.splits; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(a.part + ((long long)s * a.nr * a.H + row) * a.D + c);
+    acc[0] += v.x; acc[1] += v.y; acc[2] += v.z; acc[3] += v.w;
+  }
+  store_pack<T, 4>(static_cast<T*>(a.qb) + row * a.D + c, acc);
+}
+
+// Position gradients, one warp per node: a receiver's parts and heads, a
+// sender's key heads, or both where the senders are the receivers.
+__global__ void __launch_bounds__(256) attn_pos_kernel(AttnArgs a, bool recv, bool send, int n, float* __restrict__ bar) {
+  const int lane = threadIdx.x & 31;
+  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= n) return;
+  float x = 0.f, y = 0.f, z = 0.f;
+  if (recv)
+    for (int e = lane; e < a.splits * a.H; e += 32) {
+      const int sp = e / a.H;
+      const float4 v = a.rowpart[((long long)sp * a.nr + i) * a.H + (e - sp * a.H)];
+      x += v.x; y += v.y; z += v.z;
+    }
+  if (send)
+    for (int e = lane; e < a.KV; e += 32) {
+      const float4 v = a.colpart[(long long)e * a.ns + i];
+      x += v.x; y += v.y; z += v.z;
+    }
+  for (int o = 16; o > 0; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+    z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
+  if (lane == 0) {
+    bar[3 * i] = x; bar[3 * i + 1] = y; bar[3 * i + 2] = z;
+  }
+}
+
+// Slope gradient of one head per block, summed in FP64: the terms of a row
+// cancel, and there is one for every row.
+__global__ void __launch_bounds__(256) attn_slope_kernel(AttnArgs a, float* __restrict__ bar) {
+  __shared__ double sum[8];
+  const int h = blockIdx.x;
+  double v = 0.0;
+  for (int s = 0; s < a.splits; ++s)
+#pragma unroll 4
+    for (long long i = threadIdx.x; i < a.nr; i += 256) v += a.rowpart[((long long)s * a.nr + i) * a.H + h].w;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) v += sum[w];
+    bar[h] = (float)v;
+  }
+}
+
+// ----------------------------------------------------------------- launches
+
+struct VjpLayout {
+  int splits;
+  size_t stat, part, rowpart, colpart, bytes;
+};
+static VjpLayout vjp_layout(const fc_attn_desc* d, int B, int nr, int ns) {
+  VjpLayout l;
+  l.splits = attn_splits(B, nr, ns, d->heads / d->kv_heads, d->kv_heads, 64);
+  const size_t rows = (size_t)nr * d->heads;
+  l.stat = 0;
+  l.rowpart = round16(rows * sizeof(float2));
+  l.colpart = l.rowpart + rows * l.splits * sizeof(float4);
+  l.part = l.colpart + (size_t)ns * d->kv_heads * sizeof(float4);
+  l.bytes = l.part + (l.splits > 1 ? round16(rows * l.splits * d->head_dim * sizeof(float)) : 0);
+  return l;
+}
+
+struct VjpWants {
+  bool q, kv, pos_r, pos_s, self;
+  float *pos_recv_bar, *pos_send_bar, *slope_bar;
+};
+
+template <class T, int DP>
+static int run_vjp(const AttnArgs& a, const VjpWants& w, const float* o32, float2* stat, cudaStream_t s) {
+  static DeviceFlags ready_q, ready_kv;
+  constexpr size_t bytes = VjpSmem<T, DP>::bytes;
+  if (set_smem_once(ready_q, attn_vjp_q_kernel<T, DP>, bytes) != FC_OK ||
+      set_smem_once(ready_kv, attn_vjp_kv_kernel<T, DP>, bytes) != FC_OK)
+    return FC_ERR_CUDA;
+  if (a.nr > 0)
+    attn_stat_kernel<T><<<(unsigned)(((long long)a.nr * a.H + 31) / 32), 256, 0, s>>>(a, o32, a.lse, stat);
+  if (a.nr > 0 && (a.qb || w.pos_recv_bar || w.slope_bar)) {
+    attn_vjp_q_kernel<T, DP><<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, 64), a.KV, a.splits), 128, bytes, s>>>(a);
+    if (a.qb && a.splits > 1)
+      attn_vjp_join_kernel<T><<<(unsigned)(((long long)a.nr * a.H + 7) / 8), 256, 0, s>>>(a);
+  }
+  if (a.ns > 0 && w.kv)
+    attn_vjp_kv_kernel<T, DP><<<dim3((unsigned)tile_slots(a.B, a.ns, 1, 64), a.KV), 128, bytes, s>>>(a);
+  if (w.pos_recv_bar && a.nr > 0)
+    attn_pos_kernel<<<(unsigned)(((long long)a.nr + 7) / 8), 256, 0, s>>>(a, true, w.self, a.nr, w.pos_recv_bar);
+  if (w.pos_send_bar && a.ns > 0)
+    attn_pos_kernel<<<(unsigned)(((long long)a.ns + 7) / 8), 256, 0, s>>>(a, false, true, a.ns, w.pos_send_bar);
+  if (w.slope_bar) attn_slope_kernel<<<a.H, 256, 0, s>>>(a, w.slope_bar);
+  return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
+}
+
+template <class T>
+static int run_vjp_type(const AttnArgs& a, const VjpWants& w, const float* o32, float2* stat, cudaStream_t s) {
+  switch (attn_pad(a.D)) {
+    case 32: return run_vjp<T, 32>(a, w, o32, stat, s);
+    case 64: return run_vjp<T, 64>(a, w, o32, stat, s);
+    default: return run_vjp<T, 128>(a, w, o32, stat, s);
+  }
+}
+
+}  // namespace fc
+
+using namespace fc;
+
+extern "C" {
+
+size_t fc_node_attention_vjp_workspace_size(const fc_attn_desc* desc, int n_struct, int n_recv, int n_send) {
+  if (check_attn(desc, n_struct, n_recv, n_send) != FC_OK || (n_recv == 0 && n_send == 0)) return 0;
+  return vjp_layout(desc, n_struct, n_recv, n_send).bytes;
+}
+
+int fc_node_attention_vjp(const fc_attn_desc* desc, int n_struct, int n_recv, int n_send, const int32_t* recv_ptr,
+                          const int32_t* send_ptr, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                          const void* v, int64_t ldv, const float* pos_recv, const float* pos_send,
+                          const float* slope, const uint8_t* send_mask, const float* out_f32, const float* lse,
+                          const void* g, int64_t ldg, void* q_bar, void* k_bar, void* v_bar, float* pos_recv_bar,
+                          float* pos_send_bar, float* slope_bar, void* workspace, size_t ws_bytes,
+                          fc_stream_t stream) {
+  const int st = check_attn(desc, n_struct, n_recv, n_send);
+  if (st != FC_OK) return st;
+  const int D = desc->head_dim, H = desc->heads, KV = desc->kv_heads;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (!pos_recv != !slope || (pos_send && !pos_recv)) return FC_ERR_ARG;
+  if (pos_recv && !pos_send && n_recv != n_send) return FC_ERR_ARG;
+  if (!pos_recv && (pos_recv_bar || slope_bar)) return FC_ERR_ARG;
+  if (!pos_send && pos_send_bar) return FC_ERR_ARG;
+  if (!aligned4(slope_bar)) return FC_ERR_ALIGN;
+  if (n_recv == 0 && n_send == 0) {
+    if (slope_bar && cudaMemsetAsync(slope_bar, 0, sizeof(float) * H, s) != cudaSuccess) return FC_ERR_CUDA;
+    return FC_OK;
+  }
+  if (!recv_ptr || !send_ptr || (n_recv > 0 && (!q || !g || !out_f32 || !lse)) || (n_send > 0 && (!k || !v)))
+    return FC_ERR_ARG;
+  if ((n_recv > 0 && (ldq < (int64_t)H * D || ldg < (int64_t)H * D)) ||
+      (n_send > 0 && (ldk < (int64_t)KV * D || ldv < (int64_t)KV * D)))
+    return FC_ERR_ARG;
+  if (!aligned16(q) || !aligned16(g) || !aligned16(k) || !aligned16(v) || !aligned16(out_f32) || !aligned16(q_bar) ||
+      !aligned16(k_bar) || !aligned16(v_bar) || ldq % 8 || ldk % 8 || ldv % 8 || ldg % 8 || !aligned4(recv_ptr) ||
+      !aligned4(send_ptr) || !aligned4(pos_recv) || !aligned4(pos_send) || !aligned4(slope) || !aligned4(lse) ||
+      !aligned4(pos_recv_bar) || !aligned4(pos_send_bar))
+    return FC_ERR_ALIGN;
+  const VjpLayout l = vjp_layout(desc, n_struct, n_recv, n_send);
+  if (!workspace || ws_bytes < l.bytes) return FC_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return FC_ERR_ALIGN;
+  if (tile_slots(n_struct, n_recv, H / KV, 64) > INT32_MAX || tile_slots(n_struct, n_send, 1, 64) > INT32_MAX)
+    return FC_ERR_ARG;
+  char* ws = static_cast<char*>(workspace);
+  float2* stat = reinterpret_cast<float2*>(ws + l.stat);
+  VjpWants w{};
+  w.self = pos_recv && !pos_send;
+  w.pos_recv_bar = pos_recv_bar;
+  w.pos_send_bar = pos_send_bar;
+  w.slope_bar = slope_bar;
+  w.kv = k_bar || v_bar || pos_send_bar || (w.self && pos_recv_bar);
+  AttnArgs a{};
+  a.B = n_struct; a.nr = n_recv; a.ns = n_send; a.H = H; a.KV = KV; a.G = H / KV; a.D = D;
+  a.scale = desc->scale; a.cap = desc->cap;
+  a.ldq = ldq; a.ldk = ldk; a.ldv = ldv; a.ldg = ldg;
+  a.recv_ptr = recv_ptr; a.send_ptr = send_ptr; a.q = q; a.k = k; a.v = v; a.g = g;
+  a.pos_r = pos_recv; a.pos_s = pos_send ? pos_send : pos_recv; a.slope = slope; a.mask = send_mask;
+  a.lse = const_cast<float*>(lse);
+  a.splits = l.splits;
+  a.stat = stat;
+  a.rowpart = pos_recv_bar || slope_bar ? reinterpret_cast<float4*>(ws + l.rowpart) : nullptr;
+  a.colpart = pos_send_bar || (w.self && pos_recv_bar) ? reinterpret_cast<float4*>(ws + l.colpart) : nullptr;
+  a.part = reinterpret_cast<float*>(ws + l.part);
+  a.qb = q_bar; a.kb = k_bar; a.vb = v_bar;
+  if (desc->dtype == FC_F32) return run_vjp_type<float>(a, w, out_f32, stat, s);
+  if (desc->dtype == FC_BF16) return run_vjp_type<__nv_bfloat16>(a, w, out_f32, stat, s);
+  return run_vjp_type<__half>(a, w, out_f32, stat, s);
+}
+
+}  // extern "C"

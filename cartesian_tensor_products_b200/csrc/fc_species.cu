@@ -1,0 +1,410 @@
+// Species embedding and its gradient.
+//
+// Forward: x[n, rank 0, :] = scale table[species[n]], other ranks zero.  Bound
+// by the bytes written ((lmax+1)^2 C values per node); the table stays in L2.
+// One thread moves 16-byte vectors, a block a run of whole rows.
+//
+// Gradient: table_bar[s] = scale sum of g over the nodes of species s.  The
+// nodes are sorted by species (stable radix sort, one pass of 8 bits for
+// tables below 255 rows), the sorted list is cut into spans of 32 nodes, one
+// warp sums each span and writes the species that lie inside it; a species
+// that crosses spans leaves one partial row per span, which a last kernel adds
+// in span order.  So a species with nearly all nodes costs no more than an
+// even spread, and no sum depends on the order of atomics.
+#include <math.h>
+
+#include "fc_nodes.cuh"
+
+namespace fc {
+
+constexpr int kDigits = 256;
+constexpr int kSpan = 32;
+
+// ------------------------------------------------------------------ forward
+
+template <class T>
+__global__ void __launch_bounds__(256) species_embed_kernel(int n, int V, int vec0, int rowvec, int rows, float scale,
+                                                            const int32_t* __restrict__ species,
+                                                            const T* __restrict__ table, T* __restrict__ x) {
+  constexpr int W = RowType<T>::kVec;
+  const long long r0 = (long long)blockIdx.x * rows;
+  const int here = (int)(n - r0 < rows ? n - r0 : rows);
+  const int total = here * rowvec;
+  T* out = x + r0 * rowvec * W;
+  for (int i = threadIdx.x; i < total; i += 256) {
+    const int r = i / rowvec, c = i - r * rowvec;
+    float v[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) v[k] = 0.0f;
+    if (c < vec0) {
+      const int s = species[r0 + r];
+      if (s >= 0 && s < V) {
+        load_pack<T, W>(table + ((long long)s * vec0 + c) * W, v);
+#pragma unroll
+        for (int k = 0; k < W; ++k) v[k] *= scale;
+      }
+    }
+    store_pack<T, W>(out + (long long)i * W, v);
+  }
+}
+
+// --------------------------------------------------------------------- sort
+
+// Chunks of the sort: `rows` nodes each (a multiple of 256), at most 512.
+struct SortGeom {
+  int n, V, rows, chunks, passes;
+};
+static SortGeom sort_geom(int n, int V) {
+  SortGeom g{n, V, 1024, 0, 1};
+  const long long per = ((long long)n + 511) / 512;
+  if (per > g.rows) g.rows = (int)((per + 255) / 256 * 256);
+  g.chunks = (int)(((long long)n + g.rows - 1) / g.rows);
+  while (g.passes < 4 && ((long long)V >> (8 * g.passes)) != 0) ++g.passes;   // keys 0 .. V
+  return g;
+}
+
+// Sort key of node i: its species, or V if it has none.
+__device__ __forceinline__ int sort_key(const int32_t* __restrict__ keys, bool raw, long long i, int V) {
+  const int k = keys[i];
+  return raw && (k < 0 || k >= V) ? V : k;
+}
+
+// Digit counts of every chunk; the first pass also clears table_bar.
+__global__ void __launch_bounds__(256) sort_count_kernel(SortGeom g, int shift, bool raw,
+                                                         const int32_t* __restrict__ keys, int* __restrict__ counts,
+                                                         float4* __restrict__ clear, long long clear_n) {
+  __shared__ int hist[kDigits];
+  hist[threadIdx.x] = 0;
+  __syncthreads();
+  const long long b = (long long)blockIdx.x * g.rows;
+  const long long e = b + g.rows < g.n ? b + g.rows : g.n;
+  for (long long i = b + threadIdx.x; i < e; i += 256)
+    atomicAdd(&hist[(sort_key(keys, raw, i, g.V) >> shift) & 255], 1);
+  __syncthreads();
+  counts[blockIdx.x * kDigits + threadIdx.x] = hist[threadIdx.x];
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < clear_n; i += (long long)gridDim.x * 256)
+    clear[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
+
+// Stable scatter of one 8-bit digit: a warp owns a contiguous eighth of the
+// chunk and ranks 32 nodes at a time among equal digits.
+__global__ void __launch_bounds__(256) sort_scatter_kernel(SortGeom g, int shift, bool raw,
+                                                           const int32_t* __restrict__ keys,
+                                                           const int32_t* __restrict__ from,
+                                                           const int* __restrict__ counts, int32_t* __restrict__ okeys,
+                                                           int32_t* __restrict__ oidx) {
+  __shared__ int off[8][kDigits];
+  __shared__ int scan[kDigits];
+  const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+  int total = 0, before = 0;
+  for (int c = 0; c < g.chunks; ++c) {
+    const int v = counts[c * kDigits + t];
+    total += v;
+    if (c < (int)blockIdx.x) before += v;
+  }
+  scan[t] = total;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) off[k][t] = 0;
+  __syncthreads();
+  for (int o = 1; o < kDigits; o <<= 1) {
+    const int v = t >= o ? scan[t - o] : 0;
+    __syncthreads();
+    scan[t] += v;
+    __syncthreads();
+  }
+  const int base = scan[t] - total + before;
+  const int sub = g.rows / 8;
+  const long long b = (long long)blockIdx.x * g.rows + (long long)w * sub;
+  const long long lim = b + sub < g.n ? b + sub : g.n;
+  for (long long i = b + lane; i < lim; i += 32) atomicAdd(&off[w][(sort_key(keys, raw, i, g.V) >> shift) & 255], 1);
+  __syncthreads();
+  int run = base;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int v = off[k][t];
+    off[k][t] = run;
+    run += v;
+  }
+  __syncthreads();
+  for (long long i0 = b; i0 < lim; i0 += 32) {
+    const long long i = i0 + lane;
+    const bool live = i < lim;
+    const int key = live ? sort_key(keys, raw, i, g.V) : 0;
+    const int digit = live ? (key >> shift) & 255 : 256 + lane;
+    const unsigned peers = __match_any_sync(0xffffffffu, digit);
+    const int rank = __popc(peers & ((1u << lane) - 1u));
+    int at = 0;
+    if (live) at = off[w][digit] + rank;
+    __syncwarp();
+    if (live && rank == 0) off[w][digit] += __popc(peers);
+    __syncwarp();
+    if (live) {
+      okeys[at] = key;
+      oidx[at] = from ? from[i] : (int32_t)i;
+    }
+  }
+}
+
+// --------------------------------------------------------------------- sums
+
+// One warp: the sums of one span over one tile of 32 vectors of columns.
+template <class T>
+__global__ void __launch_bounds__(256) span_sum_kernel(int n, int V, int C, long long ldg, float scale,
+                                                       const int32_t* __restrict__ keys,
+                                                       const int32_t* __restrict__ idx, const T* __restrict__ g,
+                                                       float* __restrict__ bar, float* __restrict__ part) {
+  constexpr int W = RowType<T>::kVec;
+  const int lane = threadIdx.x & 31;
+  const long long span = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long start = span * kSpan;
+  if (start >= n) return;
+  const int cnt = (int)(n - start < kSpan ? n - start : kSpan);
+  const int col = (blockIdx.y * 32 + lane) * W;
+  const bool in = col < C;
+  const int key = lane < cnt ? keys[start + lane] : -1;
+  const int row = lane < cnt ? idx[start + lane] : 0;
+  const int prev = start > 0 ? keys[start - 1] : -1;
+  const int next = start + cnt < n ? keys[start + cnt] : -1;
+  float acc[W];
+  int cur = -1;
+  bool begins = false;
+  auto flush = [&](bool ends) {
+    if (cur < 0 || cur >= V || !in) return;
+    float* to = begins && ends ? bar + (long long)cur * C : part + (2 * span + (begins ? 1 : 0)) * C;
+    const float f = begins && ends ? scale : 1.0f;
+#pragma unroll
+    for (int k = 0; k < W; k += 4)
+      *reinterpret_cast<float4*>(to + col + k) = make_float4(acc[k] * f, acc[k + 1] * f, acc[k + 2] * f, acc[k + 3] * f);
+  };
+  constexpr int U = 8;   // rows in flight per lane
+  for (int r0 = 0; r0 < cnt; r0 += U) {
+    float v[U][W];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int rr = __shfl_sync(0xffffffffu, row, r0 + u);
+#pragma unroll
+      for (int k = 0; k < W; ++k) v[u][k] = 0.0f;
+      if (in && r0 + u < cnt) load_pack<T, W>(g + rr * ldg + col, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = __shfl_sync(0xffffffffu, key, r0 + u);
+      if (r0 + u < cnt) {
+        if (k != cur || r0 + u == 0) {
+          flush(true);
+          cur = k;
+          begins = r0 + u > 0 || prev != k;
+#pragma unroll
+          for (int i = 0; i < W; ++i) acc[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) acc[i] += v[u][i];
+      }
+    }
+  }
+  flush(next != cur);
+}
+
+// Joins the species that cross spans.  A warp looks at one span: if a species
+// begins in it and runs on, the warp adds its partial rows (at most 64 spans;
+// longer ones are added by the whole block).
+__global__ void __launch_bounds__(1024) span_join_kernel(int n, int V, int C, float scale,
+                                                         const int32_t* __restrict__ keys,
+                                                         const float* __restrict__ part, float* __restrict__ bar) {
+  __shared__ int lng[32];
+  __shared__ float sum[32][128];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long spans = ((long long)n + kSpan - 1) / kSpan;
+  const long long s = (long long)blockIdx.x * 32 + w;
+  const int col = blockIdx.y * 128 + lane * 4;
+  const bool in = col < C;
+  auto head = [&](long long sp) { return keys[sp * kSpan]; };
+  auto add = [&](float4& a, long long slot) {
+    const float4 v = *reinterpret_cast<const float4*>(part + slot * C + col);
+    a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+  };
+  if (lane == 0) lng[w] = 0;
+  int k = -1;
+  if (s + 1 < spans) {
+    k = keys[(s + 1) * kSpan - 1];
+    const bool runs_on = head(s + 1) == k;
+    const bool begins = head(s) != k || s == 0 || keys[s * kSpan - 1] != k;
+    if (!runs_on || !begins || k >= V) k = -1;
+  }
+  if (k >= 0) {
+    int m = 0;   // spans after s that start with k
+    bool open = true;
+    for (int round = 0; round < 2 && open; ++round) {
+      const long long sp = s + 1 + m + lane;
+      const unsigned same = __ballot_sync(0xffffffffu, sp < spans && head(sp < spans ? sp : 0) == k);
+      const int run = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+      m += run;
+      open = run == 32;
+    }
+    if (open) {
+      if (lane == 0) lng[w] = 1;
+    } else if (in) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      add(a, 2 * s + 1);
+#pragma unroll 4
+      for (int i = 1; i <= m; ++i) add(a, 2 * (s + i));
+      *reinterpret_cast<float4*>(bar + (long long)k * C + col) =
+          make_float4(a.x * scale, a.y * scale, a.z * scale, a.w * scale);
+    }
+  }
+  __syncthreads();
+  for (int j = 0; j < 32; ++j) {
+    if (!lng[j]) continue;
+    const long long sj = (long long)blockIdx.x * 32 + j;
+    const int kj = keys[(sj + 1) * kSpan - 1];
+    long long m = 0;
+    int run = 1024;
+    while (run == 1024) {
+      const long long sp = sj + 1 + m + threadIdx.x;
+      run = __syncthreads_count(sp < spans && head(sp < spans ? sp : 0) == kj);
+      m += run;
+    }
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) {
+      if (w == 0) add(a, 2 * sj + 1);
+#pragma unroll 8
+      for (long long i = 1 + w; i <= m; i += 32) add(a, 2 * (sj + i));
+    }
+    *reinterpret_cast<float4*>(&sum[w][lane * 4]) = a;
+    __syncthreads();
+    if (threadIdx.x < 128 && blockIdx.y * 128 + threadIdx.x < C) {
+      float v = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 32; ++q) v += sum[q][threadIdx.x];
+      bar[(long long)kj * C + blockIdx.y * 128 + threadIdx.x] = v * scale;
+    }
+    __syncthreads();
+  }
+}
+
+// ----------------------------------------------------------------- launches
+
+struct EmbedLayout {
+  SortGeom g;
+  size_t keys[2], idx[2], counts, part, bytes;
+};
+static EmbedLayout embed_layout(int n, int V, int C) {
+  EmbedLayout l;
+  l.g = sort_geom(n, V);
+  size_t at = 0;
+  const size_t list = round16(4 * (size_t)n);
+  for (int i = 0; i < 2; ++i) {
+    l.keys[i] = at;
+    at += i == 0 || l.g.passes > 1 ? list : 0;
+    l.idx[i] = at;
+    at += i == 0 || l.g.passes > 1 ? list : 0;
+  }
+  l.counts = at;
+  at += 4 * (size_t)kDigits * l.g.chunks;
+  l.part = at;
+  at += 2 * (((size_t)n + kSpan - 1) / kSpan) * C * 4;
+  l.bytes = at;
+  return l;
+}
+
+static int check_embed(int dtype, int n, int V, int lmax, int C, float scale) {
+  if (!row_dtype(dtype) || n < 0 || V < 1 || V == INT32_MAX || lmax < 0 || lmax > 8 || C <= 0 || !isfinite(scale))
+    return FC_ERR_ARG;
+  if (C > (1 << 20)) return FC_ERR_ARG;
+  if (C % (dtype == FC_F32 ? 4 : 8)) return FC_ERR_ALIGN;
+  return FC_OK;
+}
+
+template <class T>
+static int embed_fwd(int n, int V, int lmax, int C, float scale, const int32_t* species, const void* table, void* x,
+                     cudaStream_t s) {
+  constexpr int W = RowType<T>::kVec;
+  const int vec0 = C / W, rowvec = vec0 * (lmax + 1) * (lmax + 1);
+  // about 2048 vectors (32 KB) a block, fewer while that leaves SMs idle
+  int rows = 2048 / rowvec;
+  const int even = n / (4 * device_sm_count());
+  if (rows > even) rows = even;
+  if (rows < 1) rows = 1;
+  const int blocks = (int)(((long long)n + rows - 1) / rows);
+  species_embed_kernel<T><<<blocks, 256, 0, s>>>(n, V, vec0, rowvec, rows, scale, species,
+                                                 static_cast<const T*>(table), static_cast<T*>(x));
+  return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
+}
+
+template <class T>
+static void span_sum(const EmbedLayout& l, int C, long long ldg, float scale, const int32_t* keys, const int32_t* idx,
+                     const void* g, float* bar, float* part, cudaStream_t s) {
+  const long long spans = ((long long)l.g.n + kSpan - 1) / kSpan;
+  const int tile = 32 * RowType<T>::kVec;
+  span_sum_kernel<T><<<dim3((unsigned)((spans + 7) / 8), (C + tile - 1) / tile), 256, 0, s>>>(
+      l.g.n, l.g.V, C, ldg, scale, keys, idx, static_cast<const T*>(g), bar, part);
+}
+
+}  // namespace fc
+
+using namespace fc;
+
+extern "C" {
+
+int fc_species_embed(int dtype, int n_nodes, int n_species, int lmax, int channels, float scale,
+                     const int32_t* species, const void* table, void* x, fc_stream_t stream) {
+  const int st = check_embed(dtype, n_nodes, n_species, lmax, channels, scale);
+  if (st != FC_OK) return st;
+  if (n_nodes == 0) return FC_OK;
+  if (!species || !table || !x) return FC_ERR_ARG;
+  if (!aligned4(species) || !aligned16(table) || !aligned16(x)) return FC_ERR_ALIGN;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == FC_F32) return embed_fwd<float>(n_nodes, n_species, lmax, channels, scale, species, table, x, s);
+  if (dtype == FC_BF16)
+    return embed_fwd<__nv_bfloat16>(n_nodes, n_species, lmax, channels, scale, species, table, x, s);
+  return embed_fwd<__half>(n_nodes, n_species, lmax, channels, scale, species, table, x, s);
+}
+
+size_t fc_species_embed_vjp_workspace_size(int n_nodes, int n_species, int channels) {
+  if (n_nodes <= 0 || n_species < 1 || n_species == INT32_MAX || channels <= 0 || channels > (1 << 20)) return 0;
+  return embed_layout(n_nodes, n_species, channels).bytes;
+}
+
+int fc_species_embed_vjp(int dtype, int n_nodes, int n_species, int lmax, int channels, float scale,
+                         const int32_t* species, const void* g, float* table_bar, void* workspace, size_t ws_bytes,
+                         fc_stream_t stream) {
+  const int st = check_embed(dtype, n_nodes, n_species, lmax, channels, scale);
+  if (st != FC_OK) return st;
+  if (!table_bar || (n_nodes > 0 && (!species || !g))) return FC_ERR_ARG;
+  if (!aligned16(table_bar) || (n_nodes > 0 && (!aligned4(species) || !aligned16(g)))) return FC_ERR_ALIGN;
+  cudaStream_t s = (cudaStream_t)stream;
+  const size_t bar_bytes = sizeof(float) * (size_t)n_species * channels;
+  if (n_nodes == 0)
+    return cudaMemsetAsync(table_bar, 0, bar_bytes, s) == cudaSuccess ? FC_OK : FC_ERR_CUDA;
+  const EmbedLayout l = embed_layout(n_nodes, n_species, channels);
+  if (!workspace || ws_bytes < l.bytes) return FC_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return FC_ERR_ALIGN;
+  char* ws = static_cast<char*>(workspace);
+  int* counts = reinterpret_cast<int*>(ws + l.counts);
+  float* part = reinterpret_cast<float*>(ws + l.part);
+  const int32_t* keys = species;
+  const int32_t* idx = nullptr;
+  for (int p = 0; p < l.g.passes; ++p) {
+    int32_t* okeys = reinterpret_cast<int32_t*>(ws + l.keys[p & 1]);
+    int32_t* oidx = reinterpret_cast<int32_t*>(ws + l.idx[p & 1]);
+    sort_count_kernel<<<l.g.chunks, 256, 0, s>>>(l.g, 8 * p, p == 0, keys, counts, reinterpret_cast<float4*>(table_bar),
+                                                 p == 0 ? (long long)(bar_bytes / 16) : 0);
+    sort_scatter_kernel<<<l.g.chunks, 256, 0, s>>>(l.g, 8 * p, p == 0, keys, idx, counts, okeys, oidx);
+    keys = okeys;
+    idx = oidx;
+  }
+  const long long ldg = (long long)(lmax + 1) * (lmax + 1) * channels;
+  if (dtype == FC_F32)
+    span_sum<float>(l, channels, ldg, scale, keys, idx, g, table_bar, part, s);
+  else if (dtype == FC_BF16)
+    span_sum<__nv_bfloat16>(l, channels, ldg, scale, keys, idx, g, table_bar, part, s);
+  else
+    span_sum<__half>(l, channels, ldg, scale, keys, idx, g, table_bar, part, s);
+  const long long spans = ((long long)n_nodes + kSpan - 1) / kSpan;
+  if (spans > 1)
+    span_join_kernel<<<dim3((unsigned)((spans + 31) / 32), (channels + 127) / 128), 1024, 0, s>>>(
+        n_nodes, n_species, channels, scale, keys, part, table_bar);
+  return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -9,6 +9,7 @@ library has not been built this module raises on import.
 Conventions (layouts, path order, component order) are those of the header.
 """
 import ctypes as ct
+import functools
 import os
 
 import torch
@@ -42,6 +43,16 @@ class ConvDesc(ct.Structure):
 
 class LadderDesc(ct.Structure):
     _fields_ = [("lmax", ct.c_int), ("channels", ct.c_int), ("order", ct.c_int)]
+
+
+class HeadDesc(ct.Structure):
+    _fields_ = [("dtype", ct.c_int), ("heads_q", ct.c_int), ("heads_k", ct.c_int),
+                ("head_dim", ct.c_int), ("pairs", ct.c_int), ("eps", ct.c_float)]
+
+
+class AttnDesc(ct.Structure):
+    _fields_ = [("dtype", ct.c_int), ("heads", ct.c_int), ("kv_heads", ct.c_int),
+                ("head_dim", ct.c_int), ("scale", ct.c_float), ("cap", ct.c_float)]
 
 
 _vp = ct.c_void_p
@@ -89,6 +100,24 @@ _SIGS = {
     "fc_full_ladder_vjp_workspace_size": (ct.c_size_t, [ct.POINTER(LadderDesc), ct.c_int]),
     "fc_full_ladder_vjp": (ct.c_int, [ct.POINTER(LadderDesc), ct.c_int] + [_vp] * 9
                            + [ct.c_size_t, _vp]),
+    "fc_species_embed": (ct.c_int, [ct.c_int] * 5 + [ct.c_float] + [_vp] * 4),
+    "fc_species_embed_vjp_workspace_size": (ct.c_size_t, [ct.c_int] * 3),
+    "fc_species_embed_vjp": (ct.c_int, [ct.c_int] * 5 + [ct.c_float] + [_vp] * 4
+                             + [ct.c_size_t, _vp]),
+    "fc_head_norm_rotate": (ct.c_int, [ct.POINTER(HeadDesc), ct.c_int, _vp, ct.c_int64]
+                            + [_vp] * 5 + [ct.c_int64, _vp]),
+    "fc_head_norm_rotate_vjp_workspace_size": (ct.c_size_t, [ct.POINTER(HeadDesc), ct.c_int]),
+    "fc_head_norm_rotate_vjp": (ct.c_int, [ct.POINTER(HeadDesc), ct.c_int, _vp, ct.c_int64, _vp,
+                                           ct.c_int64] + [_vp] * 5 + [ct.c_int64] + [_vp] * 4
+                                + [ct.c_size_t, _vp]),
+    "fc_node_attention_workspace_size": (ct.c_size_t, [ct.POINTER(AttnDesc)] + [ct.c_int] * 3),
+    "fc_node_attention": (ct.c_int, [ct.POINTER(AttnDesc)] + [ct.c_int] * 3 + [_vp] * 2
+                          + [_vp, ct.c_int64] * 3 + [_vp] * 4 + [_vp, ct.c_int64] + [_vp] * 3
+                          + [ct.c_size_t, _vp]),
+    "fc_node_attention_vjp_workspace_size": (ct.c_size_t, [ct.POINTER(AttnDesc)] + [ct.c_int] * 3),
+    "fc_node_attention_vjp": (ct.c_int, [ct.POINTER(AttnDesc)] + [ct.c_int] * 3 + [_vp] * 2
+                              + [_vp, ct.c_int64] * 3 + [_vp] * 6 + [_vp, ct.c_int64] + [_vp] * 7
+                              + [ct.c_size_t, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -489,3 +518,258 @@ def interaction_block(lmax, order, rowptr, edge_index, edge_vec, x, omega, path_
                              want=("r",), envelope=env, stream=stream)
     F = edge_forces(edge_index, rb, N, stream=stream)
     return energy, F, z
+
+
+# ----------------------------------------------------------------------------
+# operators on node rows (include/flashcart_nodes.h)
+
+_ROW_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _node_op(f):
+    """Runs a node operator on its first tensor's device and on `stream` (None:
+    that device's current stream).  Outputs and scratch are allocated on the
+    stream that uses them."""
+    @functools.wraps(f)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise TypeError("%s takes CUDA tensors" % f.__name__)
+        dev = first.device
+        if stream is None and dev.index == torch.cuda.current_device():
+            return f(first, *args, stream=torch.cuda.current_stream(), **kw)
+        if stream is not None and stream.device != dev:
+            raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, dev))
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return f(first, *args, stream=torch.cuda.current_stream(), **kw)
+    return call
+
+
+def _on(t, dtype, name, like, shape=None):
+    """A contiguous tensor on the device of `like`; None passes."""
+    if t is None:
+        return None
+    _dev(t, dtype, name)
+    if t.device != like.device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    return t
+
+
+def _rows(t, name, like=None, shape=None):
+    """Row step of [N][heads][head_dim] rows: the heads of a row are packed,
+    rows may be a column block of a wider array."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype not in _ROW_DTYPES:
+        raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
+    if t.dim() != 3:
+        raise ValueError("%s shape %s, expected [nodes][heads][head_dim]" % (name, tuple(t.shape)))
+    if like is not None:
+        if t.device != like.device:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
+        if t.dtype != like.dtype:
+            raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError("%s: the heads of a row must be packed" % name)
+    return t.stride(0) if n > 1 else h * d
+
+
+def _bytes(workspace, need, like):
+    """Scratch of `need` bytes: a new buffer, or the caller's with its real size."""
+    if workspace is not None and workspace.device != like.device:
+        raise ValueError("workspace is on %s, expected %s" % (workspace.device, like.device))
+    workspace, size = _scratch(workspace, need, like.device)
+    return workspace, size if workspace is not None else 0
+
+
+@_node_op
+def species_embed(species, table, lmax=0, scale=1.0, out=None, stream=None):
+    """Node features [N][(lmax+1)^2 C] of the species (int32 [N]): scale times
+    the table's row [n_species][C] in the rank-0 block, zero elsewhere.  A
+    species outside the table (padding: -1) gets a zero row."""
+    _on(species, torch.int32, "species", species)
+    if table.dtype not in _ROW_DTYPES:
+        raise TypeError("table must be float32, bfloat16 or float16, got %s" % table.dtype)
+    _on(table, table.dtype, "table", species)
+    if species.dim() != 1 or table.dim() != 2:
+        raise ValueError("species [N] and table [n_species][C] expected")
+    N, (V, C) = species.shape[0], table.shape
+    shape = (N, (lmax + 1) ** 2 * C)
+    if out is None:
+        out = torch.empty(shape, dtype=table.dtype, device=table.device)
+    else:
+        _on(out, table.dtype, "out", species, shape)
+    _check(_lib.fc_species_embed(_ROW_DTYPES[table.dtype], N, V, lmax, C, scale, _ptr(species),
+                                 _ptr(table), _ptr(out), _stream(stream)), "fc_species_embed")
+    return out
+
+
+@_node_op
+def species_embed_vjp(species, g, n_species, lmax=0, scale=1.0, workspace=None, stream=None):
+    """table_bar [n_species][C] (float32) of species_embed for the gradient g
+    [N][(lmax+1)^2 C] of its output: the rank-0 rows summed by species."""
+    _on(species, torch.int32, "species", species)
+    if g.dtype not in _ROW_DTYPES:
+        raise TypeError("g must be float32, bfloat16 or float16, got %s" % g.dtype)
+    _on(g, g.dtype, "g", species)
+    N, NY = species.shape[0], (lmax + 1) ** 2
+    if species.dim() != 1 or g.dim() != 2 or g.shape[0] != N or g.shape[1] % NY:
+        raise ValueError("g shape %s" % (tuple(g.shape),))
+    C = g.shape[1] // NY
+    bar = torch.empty((n_species, C), dtype=torch.float32, device=g.device)
+    workspace, size = _bytes(workspace, _lib.fc_species_embed_vjp_workspace_size(N, n_species, C), g)
+    _check(_lib.fc_species_embed_vjp(_ROW_DTYPES[g.dtype], N, n_species, lmax, C, scale,
+                                     _ptr(species), _ptr(g), _ptr(bar), _ptr(workspace), size,
+                                     _stream(stream)), "fc_species_embed_vjp")
+    return bar
+
+
+def _head_args(x, heads_q, gamma_q, gamma_k, pos, freq, eps):
+    ldx = _rows(x, "x")
+    N, H, D = x.shape
+    if not 0 <= heads_q <= H:
+        raise ValueError("heads_q %d of %d heads" % (heads_q, H))
+    _on(gamma_q, torch.float32, "gamma_q", x, (D,))
+    _on(gamma_k, torch.float32, "gamma_k", x, (D,))
+    if (pos is None) != (freq is None):
+        raise ValueError("pos and freq go together")
+    R = 0
+    if freq is not None:
+        R = freq.shape[-1]
+        _on(freq, torch.float32, "freq", x, (3, R))
+        _on(pos, torch.float32, "pos", x, (N, 3))
+    return ldx, HeadDesc(_ROW_DTYPES[x.dtype], heads_q, H - heads_q, D, R, eps)
+
+
+@_node_op
+def head_norm_rotate(x, heads_q, gamma_q=None, gamma_k=None, pos=None, freq=None, eps=1e-6,
+                     out=None, stream=None):
+    """RMS norm of the heads x [N][heads][head_dim] (the first heads_q are
+    queries, the rest keys; x may be a column block of a fused projection) and
+    their rotation by theta_f = pos . freq[:, f] of pairs (f, f + R), with pos
+    [N][3] and freq [3][R] (None: norm only).  Returns rows like x, packed."""
+    ldx, d = _head_args(x, heads_q, gamma_q, gamma_k, pos, freq, eps)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _check(_lib.fc_head_norm_rotate(ct.byref(d), x.shape[0], _ptr(x), ldx, _ptr(gamma_q),
+                                    _ptr(gamma_k), _ptr(pos), _ptr(freq), _ptr(out),
+                                    _rows(out, "out", x, x.shape), _stream(stream)),
+           "fc_head_norm_rotate")
+    return out
+
+
+@_node_op
+def head_norm_rotate_vjp(x, g, heads_q, gamma_q=None, gamma_k=None, pos=None, freq=None, eps=1e-6,
+                         want=("x", "gamma", "pos"), workspace=None, stream=None):
+    """(x_bar, gamma_q_bar, gamma_k_bar, pos_bar) of head_norm_rotate for the
+    gradient g of its output; entries not in `want` are None, and pos_bar is
+    None without positions."""
+    ldx, d = _head_args(x, heads_q, gamma_q, gamma_k, pos, freq, eps)
+    N, H, D = x.shape
+    ldg = _rows(g, "g", x, x.shape)
+    new = lambda shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
+    xb = new(x.shape, x.dtype) if "x" in want else None
+    gqb = new((D,)) if "gamma" in want else None
+    gkb = new((D,)) if "gamma" in want else None
+    pb = new((N, 3)) if "pos" in want and pos is not None else None
+    workspace, size = _bytes(workspace, _lib.fc_head_norm_rotate_vjp_workspace_size(ct.byref(d), N)
+                             if "gamma" in want else 0, x)
+    _check(_lib.fc_head_norm_rotate_vjp(ct.byref(d), N, _ptr(x), ldx, _ptr(g), ldg, _ptr(gamma_q),
+                                        _ptr(gamma_k), _ptr(pos), _ptr(freq), _ptr(xb), H * D,
+                                        _ptr(gqb), _ptr(gkb), _ptr(pb), _ptr(workspace), size,
+                                        _stream(stream)), "fc_head_norm_rotate_vjp")
+    return xb, gqb, gkb, pb
+
+
+def _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask, scale, cap):
+    """Checked descriptor and the arguments both directions share."""
+    ldq = _rows(q, "q")
+    nr, H, D = q.shape
+    ldk = _rows(k, "k", q)
+    ns, KV = k.shape[:2]
+    if k.shape[2] != D:
+        raise ValueError("k shape %s" % (tuple(k.shape),))
+    ldv = _rows(v, "v", q, k.shape)
+    _on(recv_ptr, torch.int32, "recv_ptr", q)
+    if recv_ptr.dim() != 1 or recv_ptr.numel() < 1:
+        raise ValueError("recv_ptr shape %s" % (tuple(recv_ptr.shape),))
+    if send_ptr is None:
+        if nr != ns:
+            raise ValueError("send_ptr is needed where senders are not the receivers")
+        send_ptr = recv_ptr
+    _on(send_ptr, torch.int32, "send_ptr", q, recv_ptr.shape)
+    if (pos is None) != (slope is None) or (pos is None and pos_send is not None):
+        raise ValueError("pos and slope go together, pos_send needs both")
+    _on(pos, torch.float32, "pos", q, (nr, 3))
+    _on(pos_send, torch.float32, "pos_send", q, (ns, 3))
+    _on(slope, torch.float32, "slope", q, (H,))
+    _on(send_mask, torch.uint8, "send_mask", q, (ns,))
+    if pos is not None and pos_send is None and nr != ns:
+        raise ValueError("pos_send is needed where senders are not the receivers")
+    if scale is None:
+        scale = D ** -0.5
+    d = AttnDesc(_ROW_DTYPES[q.dtype], H, KV, D, scale, cap)
+    sizes = (recv_ptr.shape[0] - 1, nr, ns)
+    args = (_ptr(recv_ptr), _ptr(send_ptr), _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(pos),
+            _ptr(pos_send), _ptr(slope), _ptr(send_mask))
+    return d, sizes, args
+
+
+@_node_op
+def node_attention(q, k, v, recv_ptr, send_ptr=None, pos=None, pos_send=None, slope=None,
+                   send_mask=None, scale=None, cap=0.0, residual=False, workspace=None, stream=None):
+    """(out [n_recv][heads][head_dim], lse [n_recv][heads], out_f32) of the
+    attention of q [n_recv][heads][head_dim] to k, v [n_send][kv_heads][head_dim]
+    inside each structure: receivers recv_ptr[b] .. recv_ptr[b+1], senders
+    send_ptr[b] .. (None: the receivers).  Scores scale q.k (scale None:
+    head_dim^-1/2), capped by cap tanh(. / cap) if cap > 0, minus slope[head]
+    times the distance of pos and pos_send (None: pos).  send_mask: uint8, 0
+    hides a sender.  Rows without senders are 0 with lse -inf.  out_f32, which
+    node_attention_vjp needs, is None unless residual (float32: it is out)."""
+    d, sizes, args = _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask, scale, cap)
+    nr, H, D = q.shape
+    out = torch.empty((nr, H, D), dtype=q.dtype, device=q.device)
+    lse = torch.empty((nr, H), dtype=torch.float32, device=q.device)
+    o32 = None
+    if residual:
+        o32 = out if q.dtype == torch.float32 else torch.empty((nr, H, D), dtype=torch.float32,
+                                                               device=q.device)
+    workspace, size = _bytes(workspace, _lib.fc_node_attention_workspace_size(ct.byref(d), *sizes), q)
+    _check(_lib.fc_node_attention(ct.byref(d), *sizes, *args, _ptr(out), H * D, _ptr(lse),
+                                  _ptr(o32) if o32 is not out else None, _ptr(workspace), size,
+                                  _stream(stream)), "fc_node_attention")
+    return out, lse, o32
+
+
+@_node_op
+def node_attention_vjp(q, k, v, out_f32, lse, g, recv_ptr, send_ptr=None, pos=None, pos_send=None,
+                       slope=None, send_mask=None, scale=None, cap=0.0,
+                       want=("q", "k", "v", "pos", "slope"), workspace=None, stream=None):
+    """(q_bar, k_bar, v_bar, pos_bar, pos_send_bar, slope_bar) of node_attention
+    for the gradient g of out, given the out_f32 (residual=True) and lse it
+    returned.  Without pos_send, pos_bar holds both roles of a node and
+    pos_send_bar is None; entries not in `want`, and without a bias those of
+    pos and slope, are None."""
+    d, sizes, args = _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask, scale, cap)
+    if out_f32 is None:
+        raise ValueError("out_f32 is needed: node_attention(..., residual=True) returns it")
+    _on(out_f32, torch.float32, "out_f32", q, q.shape)
+    _on(lse, torch.float32, "lse", q, q.shape[:2])
+    ldg = _rows(g, "g", q, q.shape)
+    new = lambda shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=q.device)  # noqa: E731
+    qb = new(q.shape, q.dtype) if "q" in want else None
+    kb = new(k.shape, q.dtype) if "k" in want else None
+    vb = new(v.shape, q.dtype) if "v" in want else None
+    pb = new((q.shape[0], 3)) if "pos" in want and pos is not None else None
+    psb = new((k.shape[0], 3)) if "pos" in want and pos_send is not None else None
+    sb = new((q.shape[1],)) if "slope" in want and slope is not None else None
+    workspace, size = _bytes(workspace, _lib.fc_node_attention_vjp_workspace_size(ct.byref(d), *sizes), q)
+    _check(_lib.fc_node_attention_vjp(ct.byref(d), *sizes, *args, _ptr(out_f32), _ptr(lse), _ptr(g),
+                                      ldg, _ptr(qb), _ptr(kb), _ptr(vb), _ptr(pb), _ptr(psb),
+                                      _ptr(sb), _ptr(workspace), size, _stream(stream)),
+           "fc_node_attention_vjp")
+    return qb, kb, vb, pb, psb, sb
