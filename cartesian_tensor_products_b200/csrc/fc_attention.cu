@@ -233,19 +233,28 @@ int check_attn(const fc_attn_desc* d, int n_struct, int n_recv, int n_send) {
 
 int attn_pad(int head_dim) { return head_dim <= 32 ? 32 : head_dim <= 64 ? 64 : 128; }
 
-// Parts of the key range: enough blocks for two per SM, each part at least
+// Parts of the senders: enough blocks to fill the card, each part at least
 // four product steps of an average structure.
-int attn_splits(int B, int nr, int ns, int G, int KV, int step) {
-  const long long blocks = ((long long)nr * G + 63) / 64 * KV;
+static int parts(long long blocks, long long fill, int B, int ns, int step) {
   const long long per = B > 0 ? ns / B : 0;
-  const long long want = blocks > 0 ? 2LL * device_sm_count() / blocks : 1;
-  const long long most = per / (4 * step);
+  const long long want = blocks > 0 ? fill / blocks : 1, most = per / (4 * step);
   long long s = want < most ? want : most;
   if (s > 64) s = 64;
   return s < 1 ? 1 : (int)s;
 }
 
-static int fwd_step(const fc_attn_desc* d) { return d->dtype == FC_F32 && d->head_dim > 64 ? 32 : 64; }
+#ifndef FC_TC_ROWS
+#define FC_TC_ROWS 96
+#endif
+AttnPlan attn_plan(const fc_attn_desc* d, int B, int nr, int ns) {
+  AttnPlan p;
+  const long long rows = (long long)nr * (d->heads / d->kv_heads);
+  const int sms = device_sm_count();
+  p.tc = d->dtype != FC_F32 && B > 0 && rows / B >= FC_TC_ROWS && ns / B >= 128 && rows < (1ll << 31);
+  p.splits = p.tc ? parts((rows + 127) / 128 * d->kv_heads, sms, B, ns, 64)
+                  : parts((rows + 63) / 64 * d->kv_heads, 2 * sms, B, ns, d->dtype == FC_F32 && d->head_dim > 64 ? 32 : 64);
+  return p;
+}
 
 template <class T, int DP, bool Two>
 static int run_attn(const AttnArgs& a, cudaStream_t s) {
@@ -253,19 +262,25 @@ static int run_attn(const AttnArgs& a, cudaStream_t s) {
   constexpr size_t bytes = FwdSmem<T, DP>::bytes;
   if (set_smem_once(ready, attn_fwd_kernel<T, DP, Two>, bytes) != FC_OK) return FC_ERR_CUDA;
   attn_fwd_kernel<T, DP, Two><<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, 64), a.KV, a.splits), 128, bytes, s>>>(a);
-  if (a.splits > 1)
-    attn_join_kernel<T><<<(unsigned)(((long long)a.nr * a.H + 7) / 8), 256, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
 }
 
 template <class T>
-static int run_attn_type(const AttnArgs& a, cudaStream_t s) {
+static int run_strips(const AttnArgs& a, cudaStream_t s) {
   const bool two = sizeof(T) == 2 && a.o32;
   switch (attn_pad(a.D)) {
     case 32: return two ? run_attn<T, 32, sizeof(T) == 2>(a, s) : run_attn<T, 32, false>(a, s);
     case 64: return two ? run_attn<T, 64, sizeof(T) == 2>(a, s) : run_attn<T, 64, false>(a, s);
     default: return two ? run_attn<T, 128, sizeof(T) == 2>(a, s) : run_attn<T, 128, false>(a, s);
   }
+}
+
+template <class T>
+static int run_attn_type(int dtype, bool tc, const AttnArgs& a, cudaStream_t s) {
+  const int rc = tc ? launch_attn_fwd_tc(dtype, a, s) : run_strips<T>(a, s);
+  if (rc != FC_OK || a.splits == 1) return rc;
+  attn_join_kernel<T><<<(unsigned)(((long long)a.nr * a.H + 7) / 8), 256, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
 }
 
 }  // namespace fc
@@ -276,7 +291,7 @@ extern "C" {
 
 size_t fc_node_attention_workspace_size(const fc_attn_desc* desc, int n_struct, int n_recv, int n_send) {
   if (check_attn(desc, n_struct, n_recv, n_send) != FC_OK || n_recv == 0) return 0;
-  const int sp = attn_splits(n_struct, n_recv, n_send, desc->heads / desc->kv_heads, desc->kv_heads, fwd_step(desc));
+  const int sp = attn_plan(desc, n_struct, n_recv, n_send).splits;
   if (sp == 1) return 0;
   const size_t rows = (size_t)sp * n_recv * desc->heads;
   return round16(rows * desc->head_dim * sizeof(float)) + round16(rows * sizeof(float2));
@@ -307,7 +322,8 @@ int fc_node_attention(const fc_attn_desc* desc, int n_struct, int n_recv, int n_
   a.recv_ptr = recv_ptr; a.send_ptr = send_ptr; a.q = q; a.k = k; a.v = v;
   a.pos_r = pos_recv; a.pos_s = pos_send ? pos_send : pos_recv; a.slope = slope; a.mask = send_mask;
   a.out = out; a.lse = lse; a.o32 = out_f32;
-  a.splits = attn_splits(n_struct, n_recv, n_send, a.G, KV, fwd_step(desc));
+  const AttnPlan plan = attn_plan(desc, n_struct, n_recv, n_send);
+  a.splits = plan.splits;
   if (tile_slots(a.B, a.nr, a.G, 64) > INT32_MAX) return FC_ERR_ARG;
   if (a.splits > 1) {
     const size_t need = fc_node_attention_workspace_size(desc, n_struct, n_recv, n_send);
@@ -318,9 +334,9 @@ int fc_node_attention(const fc_attn_desc* desc, int n_struct, int n_recv, int n_
                                           round16((size_t)a.splits * n_recv * H * D * sizeof(float)));
   }
   cudaStream_t s = (cudaStream_t)stream;
-  if (desc->dtype == FC_F32) return run_attn_type<float>(a, s);
-  if (desc->dtype == FC_BF16) return run_attn_type<__nv_bfloat16>(a, s);
-  return run_attn_type<__half>(a, s);
+  if (desc->dtype == FC_F32) return run_attn_type<float>(FC_F32, false, a, s);
+  if (desc->dtype == FC_BF16) return run_attn_type<__nv_bfloat16>(FC_BF16, plan.tc, a, s);
+  return run_attn_type<__half>(FC_F16, plan.tc, a, s);
 }
 
 }  // extern "C"

@@ -116,6 +116,8 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" : : "n"(N) : "memory");
 }
 
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Row stride of a shared tile in values: 16 bytes more than the row, so that
 // eight rows at one column start in eight different 16-byte bank groups.
 template <class T, int DP>
@@ -320,9 +322,16 @@ __device__ __forceinline__ void strip_pn(float (&acc)[DP / 8][4], const float (&
 template <class T, int DP>
 constexpr int kStep = sizeof(T) == 4 && DP > 64 ? 32 : 64;
 
-// Geometry of the calls (fc_attention.cu), shared by both directions.
+// How a call runs (fc_attention.cu): on the tcgen05 kernels or the strip
+// kernels, and in how many parts of the senders (forward, query gradient).
+struct AttnPlan {
+  bool tc;
+  int splits;
+};
 int check_attn(const fc_attn_desc* d, int n_struct, int n_recv, int n_send);
-int attn_splits(int B, int nr, int ns, int G, int KV, int step);
+AttnPlan attn_plan(const fc_attn_desc* d, int n_struct, int n_recv, int n_send);
 int attn_pad(int head_dim);
+// fc_attention_tc.cu: 16-bit types
+int launch_attn_fwd_tc(int dtype, const AttnArgs& a, cudaStream_t s);
 
 }  // namespace fc

@@ -407,7 +407,7 @@ struct VjpLayout {
 };
 static VjpLayout vjp_layout(const fc_attn_desc* d, int B, int nr, int ns) {
   VjpLayout l;
-  l.splits = attn_splits(B, nr, ns, d->heads / d->kv_heads, d->kv_heads, 64);
+  l.splits = attn_plan(d, B, nr, ns).splits;
   const size_t rows = (size_t)nr * d->heads;
   l.stat = 0;
   l.rowpart = round16(rows * sizeof(float2));

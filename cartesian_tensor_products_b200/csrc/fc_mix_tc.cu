@@ -1256,15 +1256,22 @@ int launch_path_mix_tc(const PathGeom& g, const float* xs, const float* ws, floa
 
 }  // namespace fc
 
+// the same two for the attention kernels' word and bound (fc_attention_tc.cu)
+namespace fc {
+int attn_tc_take_error(int* flag, cudaStream_t s);
+int attn_tc_set_wait(unsigned long long ns);
+}  // namespace fc
+
 extern "C" int fc_device_error(int* flag, fc_stream_t stream) {
   if (!flag) return FC_ERR_ARG;
   cudaStream_t s = (cudaStream_t)stream;
-  int h = 0;
+  int h = 0, at = 0;
   if (cudaMemcpyFromSymbolAsync(&h, fc::g_tc_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
           cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess)
     return FC_ERR_CUDA;
-  *flag = h;
+  if (fc::attn_tc_take_error(&at, s) != FC_OK) return FC_ERR_CUDA;
+  *flag = h | at;
   if (h) {
     const int zero = 0;
     if (cudaMemcpyToSymbolAsync(fc::g_tc_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
@@ -1278,5 +1285,5 @@ extern "C" int fc_device_error(int* flag, fc_stream_t stream) {
 extern "C" int fc_set_wait_timeout(uint64_t ns) {
   const unsigned long long v = ns ? (unsigned long long)ns : fc::kTcDefaultWaitNs;
   if (cudaMemcpyToSymbol(fc::g_tc_wait_ns, &v, sizeof(v)) != cudaSuccess) return FC_ERR_CUDA;
-  return FC_OK;
+  return fc::attn_tc_set_wait(v);
 }

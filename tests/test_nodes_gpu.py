@@ -235,6 +235,11 @@ class Case:
             far = 4 * 3 ** 0.5 if n == "slope" else 1.0    # the largest distance
             share = float(row.sum()) if n == "slope" else float(row.sum(1).max()) * 2 if n == "pos" else float(row.sum())
             close(a, bars[n], VJP_TOL * big(bars[n]) + t * t * share * 1.5 * far)
+        if self.dtype != F32:     # without the residual the weights are one 16-bit term
+            q, k, v = self.parts(dev(self.qw), dev(self.kw))
+            one = fc.node_attention(q, k, v, dev(self.rp), send_ptr=dev(self.sp), send_mask=dev(self.mask), **self.kwargs(dev))
+            close(one[0], ref, R.u(self.dtype) * ref.abs() + t * mo + FWD_TOL * big(ref) + low)
+        assert fc.device_error() == 0
         again = self.run(fc)
         for a, b in zip([out, l, o32, *got], [*again[0], *again[1]]):
             assert (a is None and b is None) or torch.equal(a, b)
@@ -260,6 +265,10 @@ ATTN = {
     "probe split bf16": dict(recv=[2, 1, 1], send=[4000, 0, 1500], h=8, kv=2, d=128, dtype=BF16),
     "long": dict(recv=[1100], send=None, h=2, kv=1, d=64, dtype=F16, cap=3.0),
     "long f32": dict(recv=[1100], send=None, h=2, kv=2, d=64, dtype=F32),
+    # enough blocks that the senders are not split: more tiles than a block has stages
+    "many tiles": dict(recv=[1300], send=None, h=16, kv=16, d=32, dtype=BF16, cap=6.0),
+    "many tiles wide": dict(recv=[900, 650], send=None, h=16, kv=8, d=128, dtype=F16, hide=0.1),
+    "many tiles no bias": dict(recv=[1250], send=None, h=16, kv=16, d=64, dtype=BF16, bias=False),
     "many": dict(recv=[(7 * i) % 23 for i in range(300)], send=None, h=2, kv=2, d=16, dtype=F32),
 }
 
