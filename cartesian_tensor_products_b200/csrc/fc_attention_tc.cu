@@ -31,7 +31,115 @@ struct AtFwd {
   static_assert(bytes <= 232448 && col_o + 2 * DP <= 512, "shared or tensor memory");
 };
 
-template <class T, int DP, int PT>
+// The scores of one row against a tile, in base 2 and relative to a reference.
+template <class T, bool Cap, bool Bias>
+struct RowScore {
+  float2 mul, cap2, px, py, pz, sl;   // slope negated
+  TanhPoly poly;
+  __device__ __forceinline__ RowScore(const AttnArgs& a, long long node, int head)
+      : mul(pair(Cap ? a.scale / a.cap : a.scale * kLog2e)), cap2(pair(a.cap * kLog2e)), poly(a.cap * kLog2e) {
+    px = py = pz = sl = pair(0.0f);
+    if (Bias) {
+      px = pair(a.pos_r[3 * node]);
+      py = pair(a.pos_r[3 * node + 1]);
+      pz = pair(a.pos_r[3 * node + 2]);
+      sl = pair(-a.slope[head] * kLog2e);
+    }
+  }
+  // y += slope distance + (0 or -infinity), 32 columns; in: positions and flags of the tile
+  template <bool Flags>
+  __device__ __forceinline__ void bias(float2* y, const float* in) const {
+    if (Bias) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float4 fx = *reinterpret_cast<const float4*>(in + 2 * e),
+                     fy = *reinterpret_cast<const float4*>(in + kAtStep + 2 * e),
+                     fz = *reinterpret_cast<const float4*>(in + 2 * kAtStep + 2 * e);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 dx = add2(px, h ? hi2(fx) : lo2(fx)), dy = add2(py, h ? hi2(fy) : lo2(fy)),
+                       dz = add2(pz, h ? hi2(fz) : lo2(fz));
+          const float2 d2 = fma2(dx, dx, fma2(dy, dy, fma2(dz, dz, pair(kD2Seed))));
+          y[e + h] = fma2(mul2(d2, make_float2(rsq(d2.x), rsq(d2.y))), sl, y[e + h]);
+        }
+      }
+    }
+    if (Flags)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = add2(y[e], lds2(in + 3 * kAtStep + 2 * e));
+  }
+  // 64 columns with the cap's polynomial; big: the largest score over the cap
+  template <bool Flags>
+  __device__ __forceinline__ void easy(uint32_t st, const float* in, float neg_m, float2 (&x)[32], float& big) const {
+    const float2 nm = pair(neg_m);
+    uint32_t r[2][32];
+    tmem_ld32_async(st, r[0]);
+    float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      tmem_wait_ld(r[hf]);
+      if (hf == 0) tmem_ld32_async(st + 32, r[1]);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if (Cap) {
+          const float2 v = mul2(pair_at(r[hf], e), mul);
+          b[e & 3] = max3_abs(b[e & 3], v.x, v.y);
+          x[16 * hf + e] = fma2(v, poly(mul2(v, v)), nm);
+        } else {
+          x[16 * hf + e] = fma2(pair_at(r[hf], e), mul, nm);
+        }
+      }
+      bias<Flags>(x + 16 * hf, in + 32 * hf);
+    }
+    if (Cap) big = max3(fmaxf(b[0], b[1]), b[2], b[3]);
+  }
+  // any scores; whether the polynomial would have served the warp
+  __device__ __forceinline__ bool any(uint32_t st, const float* in, float neg_m, bool flags, float2 (&x)[32]) const {
+    const float2 nm = pair(neg_m);
+    bool small = true;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t r[32];
+      tmem_ld32_async(st + 32 * hf, r);
+      tmem_wait_ld(r);
+      float2 y[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = Cap ? mul2(pair_at(r, e), mul) : fma2(pair_at(r, e), mul, nm);
+      if (Cap) {
+        small &= tanh_in_range(y);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = fma2(make_float2(cap_tanh<T>(y[e].x), cap_tanh<T>(y[e].y)), cap2, nm);
+      }
+      if (flags)
+        bias<true>(y, in + 32 * hf);
+      else
+        bias<false>(y, in + 32 * hf);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[16 * hf + e] = y[e];
+    }
+    return small;
+  }
+};
+
+// The weights of 64 scores as PT 16-bit terms, and their sum.
+template <class T, int PT>
+__device__ __forceinline__ float weigh(float2 (&x)[32], uint32_t (&w)[PT][32]) {
+  float2 sum[2] = {pair(0.0f), pair(0.0f)};
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    x[e] = make_float2(ex2(x[e].x), ex2(x[e].y));
+    sum[e & 1] = add2(sum[e & 1], x[e]);
+    w[0][e] = pack2<T>(x[e].x, x[e].y);
+    if (PT == 2) {   // what the rounding left
+      const T* h = reinterpret_cast<const T*>(&w[0][e]);
+      w[PT - 1][e] = pack2<T>(x[e].x - RowType<T>::to(h[0]), x[e].y - RowType<T>::to(h[1]));
+    }
+  }
+  sum[0] = add2(sum[0], sum[1]);
+  return sum[0].x + sum[0].y;
+}
+
+template <class T, int DP, int PT, bool Cap, bool Bias>
 __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, const __grid_constant__ CUtensorMap kmap,
                                                                 const __grid_constant__ CUtensorMap vmap) {
   using L = AtFwd<DP>;
@@ -167,7 +275,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const long long j = j0 + 32 * n + lane;
-          const bool ok = j < shi && (!a.mask || a.mask[j]), there = ok && a.pos_r;
+          const bool ok = j < shi && (!a.mask || a.mask[j]), there = Bias && ok;
           float* f = info(s) + 32 * n + lane;
           f[0] = there ? -a.pos_s[3 * j] : 0.0f;
           f[kAtStep] = there ? -a.pos_s[3 * j + 1] : 0.0f;
@@ -201,20 +309,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
     const uint32_t ot = tmem + lanes + L::col_o + wg * DP;
     const uint32_t u = (uint32_t)(mine ? vr : at.v0);
     const int node = (int)(u / (uint32_t)a.G), head = kvh * a.G + (int)(u - (uint32_t)node * a.G);
-    float2 px = pair(0.f), py = px, pz = px, sl = px;   // slope negated, in base 2
-    if (a.pos_r) {
-      px = pair(a.pos_r[3ll * node]);
-      py = pair(a.pos_r[3ll * node + 1]);
-      pz = pair(a.pos_r[3ll * node + 2]);
-      sl = pair(-a.slope[head] * kLog2e);
-    }
-    const float2 mul = pair(a.cap > 0.0f ? a.scale / a.cap : a.scale * kLog2e), cap2 = pair(a.cap * kLog2e);
+    RowScore<T, Cap, Bias> score(a, node, head);
     // m: what the scores are taken relative to (base 2).  It is set by the
     // row's first score and raised only when a tile exceeds it by 2^8, so that
     // most tiles fold its subtraction into the score and need no rescaling.
     float m = 0.0f, l = 0.0f;
     bool set = false;
-    const TanhPoly poly(a.cap * kLog2e);
+    bool easy = false;   // the last tile's scores were in the polynomial's range
     int j = 0;   // tiles of this group
     for (int i = wg; i < nt; i += 2, ++j) {
       const int s = i % NST;
@@ -226,105 +327,61 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
       const uint32_t st = tmem + lanes + (i & 3) * kAtStep;
       const float* in = info(s);
       const bool ragged = a.mask || (t0 + i + 1) * (long long)kAtStep > shi - slo;
-      const float2 nm = pair(-m);
       float2 x[32];
-      uint32_t r[2][32];
-      tmem_ld32_async(st, r[0]);
+      bool done = false;
+      if (easy) {
+        // Straight through on the present reference, without a branch from the
+        // scores to the packed weights, so that one column's exp and square
+        // root overlap the next one's arithmetic; kept if nothing was out of
+        // range, else done again below.
+        float big = 0.0f;
+        if (ragged)
+          score.template easy<true>(st, in, -m, x, big);
+        else
+          score.template easy<false>(st, in, -m, x, big);
+        const float mx = max_pairs(x);
+        uint32_t w[PT][32];
+        const float sum = weigh<T, PT>(x, w);
+        if (!__any_sync(0xffffffffu, !(big <= kTanhMax) || mx > (set ? 8.0f : -INFINITY))) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {   // 32 columns at a time, the next on their way
-        tmem_wait_ld(r[hf]);
-        if (hf == 0) tmem_ld32_async(st + 32, r[1]);
-        float2 y[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = pair_at(r[hf], e);
-        if (a.cap > 0.0f) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = mul2(y[e], mul);
-          if (tanh_in_range(y)) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = fma2(y[e], poly(mul2(y[e], y[e])), nm);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              y[e] = fma2(make_float2(cap_tanh<T>(y[e].x), cap_tanh<T>(y[e].y)), cap2, nm);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = fma2(y[e], mul, nm);
+          for (int p = 0; p < PT; ++p) tc::tmem_st32(st + 32 * p, w[p]);
+          l += sum;
+          done = true;
         }
-        const float* ih = in + 32 * hf;
-        if (a.pos_r) {
+      }
+      if (!done) {
+        easy = score.any(st, in, -m, ragged, x);
+        const float mx = max_pairs(x);
+        const bool raise = mx > (set ? 8.0f : -INFINITY);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float up = raise ? mx : 0.0f;
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float4 fx = *reinterpret_cast<const float4*>(ih + 2 * e),
-                         fy = *reinterpret_cast<const float4*>(ih + kAtStep + 2 * e),
-                         fz = *reinterpret_cast<const float4*>(ih + 2 * kAtStep + 2 * e);
+          for (int e = 0; e < 32; ++e) x[e] = add2(x[e], pair(-up));
+          m += up;
+          if (j > 0) {   // rescale the sum and the output so far (0 before the row's first score)
+            const float al = set ? ex2(-up) : 1.0f;
+            l *= al;
+            if (!tc::bar_wait(&o_full[wg], (j - 1) & 1, lim)) {
+              fail = true;
+              break;
+            }
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int c = 0; c < a.D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32_async(ot + c, o);
+              tmem_wait_ld(o);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float2 dx = add2(px, h ? hi2(fx) : lo2(fx)), dy = add2(py, h ? hi2(fy) : lo2(fy)),
-                           dz = add2(pz, h ? hi2(fz) : lo2(fz));
-              const float2 d2 = fma2(dx, dx, fma2(dy, dy, fma2(dz, dz, pair(kD2Seed))));
-              y[e + h] = fma2(mul2(d2, make_float2(rsq(d2.x), rsq(d2.y))), sl, y[e + h]);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+              tc::tmem_st32(ot + c, o);
             }
           }
+          set |= raise;
         }
-        if (ragged) {
+        uint32_t w[PT][32];
+        l += weigh<T, PT>(x, w);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = add2(y[e], lds2(ih + 3 * kAtStep + 2 * e));
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[16 * hf + e] = y[e];
-      }
-      const float mx = max_pairs(x);
-      const bool raise = mx > (set ? 8.0f : -INFINITY);
-      if (__any_sync(0xffffffffu, raise)) {
-        const float up = raise ? mx : 0.0f;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = add2(x[e], pair(-up));
-        m += up;
-        if (j > 0) {   // rescale the sum and the output so far (0 before the row's first score)
-          const float al = set ? ex2(-up) : 1.0f;
-          l *= al;
-          if (!tc::bar_wait(&o_full[wg], (j - 1) & 1, lim)) {
-            fail = true;
-            break;
-          }
-          tc::fence_after_sync();
-#pragma unroll 1
-          for (int c = 0; c < a.D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32_async(ot + c, o);
-            tmem_wait_ld(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-            tc::tmem_st32(ot + c, o);
-          }
-        }
-        set |= raise;
-      }
-      float2 sum = pair(0.f), sum2 = pair(0.f);
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        x[e] = make_float2(ex2(x[e].x), ex2(x[e].y));
-        x[e + 1] = make_float2(ex2(x[e + 1].x), ex2(x[e + 1].y));
-        sum = add2(sum, x[e]);
-        sum2 = add2(sum2, x[e + 1]);
-      }
-      sum = add2(sum, sum2);
-      l += sum.x + sum.y;
-#pragma unroll
-      for (int p = 0; p < PT; ++p) {
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          w[e] = pack2<T>(x[e].x, x[e].y);
-          if (p + 1 < PT) {   // what the rounding left
-            const T* h = reinterpret_cast<const T*>(&w[e]);
-            x[e].x -= RowType<T>::to(h[0]);
-            x[e].y -= RowType<T>::to(h[1]);
-          }
-        }
-        tc::tmem_st32(st + 32 * p, w);
+        for (int p = 0; p < PT; ++p) tc::tmem_st32(st + 32 * p, w[p]);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
@@ -431,21 +488,26 @@ bool at_tensor_map(CUtensorMap* m, bool half, const void* base, int D, int heads
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class T, int DP, int PT>
+template <class T, int DP, int PT, bool Cap, bool Bias>
 static int run_fwd_tc(const AttnArgs& a, cudaStream_t s) {
   static DeviceFlags ready;
-  if (set_smem_once(ready, attn_fwd_tc_kernel<T, DP, PT>, AtFwd<DP>::bytes) != FC_OK) return FC_ERR_CUDA;
+  if (set_smem_once(ready, attn_fwd_tc_kernel<T, DP, PT, Cap, Bias>, AtFwd<DP>::bytes) != FC_OK) return FC_ERR_CUDA;
   CUtensorMap km, vm;
   constexpr bool half = __is_same(T, __half);
   if (!at_tensor_map(&km, half, a.k, a.D, a.KV, a.ldk, a.ns) || !at_tensor_map(&vm, half, a.v, a.D, a.KV, a.ldv, a.ns))
     return FC_ERR_CUDA;
-  attn_fwd_tc_kernel<T, DP, PT><<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, kAtRows), a.KV, a.splits), kAtThreads,
-                                  AtFwd<DP>::bytes, s>>>(a, km, vm);
+  attn_fwd_tc_kernel<T, DP, PT, Cap, Bias>
+      <<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, kAtRows), a.KV, a.splits), kAtThreads, AtFwd<DP>::bytes, s>>>(a, km, vm);
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
+}
+template <class T, int DP, int PT>
+static int run_fwd_terms(const AttnArgs& a, cudaStream_t s) {
+  if (a.cap > 0.0f) return a.pos_r ? run_fwd_tc<T, DP, PT, true, true>(a, s) : run_fwd_tc<T, DP, PT, true, false>(a, s);
+  return a.pos_r ? run_fwd_tc<T, DP, PT, false, true>(a, s) : run_fwd_tc<T, DP, PT, false, false>(a, s);
 }
 template <class T, int PT>
 static int run_fwd_dim(const AttnArgs& a, cudaStream_t s) {
-  return a.D <= 64 ? run_fwd_tc<T, 64, PT>(a, s) : run_fwd_tc<T, 128, PT>(a, s);
+  return a.D <= 64 ? run_fwd_terms<T, 64, PT>(a, s) : run_fwd_terms<T, 128, PT>(a, s);
 }
 
 int launch_attn_fwd_tc(int dtype, const AttnArgs& a, cudaStream_t s) {
