@@ -233,10 +233,9 @@ int check_attn(const fc_attn_desc* d, int n_struct, int n_recv, int n_send) {
 
 int attn_pad(int head_dim) { return head_dim <= 32 ? 32 : head_dim <= 64 ? 64 : 128; }
 
-// Parts of the senders: enough blocks to fill the card, each part at least
-// four product steps of an average structure.
-static int parts(long long blocks, long long fill, int B, int ns, int step) {
-  const long long per = B > 0 ? ns / B : 0;
+// Parts of the streamed side: enough blocks to fill the card, each part at
+// least four product steps of an average structure.
+static int parts(long long blocks, long long fill, long long per, int step) {
   const long long want = blocks > 0 ? fill / blocks : 1, most = per / (4 * step);
   long long s = want < most ? want : most;
   if (s > 64) s = 64;
@@ -248,11 +247,16 @@ static int parts(long long blocks, long long fill, int B, int ns, int step) {
 #endif
 AttnPlan attn_plan(const fc_attn_desc* d, int B, int nr, int ns) {
   AttnPlan p;
-  const long long rows = (long long)nr * (d->heads / d->kv_heads);
-  const int sms = device_sm_count();
-  p.tc = d->dtype != FC_F32 && B > 0 && rows / B >= FC_TC_ROWS && ns / B >= 128 && rows < (1ll << 31);
-  p.splits = p.tc ? parts((rows + 127) / 128 * d->kv_heads, sms, B, ns, 64)
-                  : parts((rows + 63) / 64 * d->kv_heads, 2 * sms, B, ns, d->dtype == FC_F32 && d->head_dim > 64 ? 32 : 64);
+  const int G = d->heads / d->kv_heads, KV = d->kv_heads, sms = device_sm_count();
+  const long long rows = (long long)nr * G, per_r = B > 0 ? rows / B : 0, per_s = B > 0 ? ns / B : 0;
+  const int step = d->dtype == FC_F32 && d->head_dim > 64 ? 32 : 64;
+  p.tc = d->dtype != FC_F32 && per_r >= FC_TC_ROWS && per_s >= 128 && rows < (1ll << 31);
+  p.tc_vjp = p.tc && G <= 64;
+  p.splits = p.tc ? parts((rows + 127) / 128 * KV, sms, per_s, 64) : parts((rows + 63) / 64 * KV, 2 * sms, per_s, step);
+  p.q_splits = p.tc_vjp ? parts((rows + 127) / 128 * KV, sms, per_s, 64)
+                        : parts((rows + 63) / 64 * KV, 2 * sms, per_s, step);
+  p.kv_splits = p.tc_vjp ? parts(((long long)ns + 127) / 128 * KV, sms, per_r, 64)
+                         : parts(((long long)ns + 63) / 64 * KV, 2 * sms, per_r, step);
   return p;
 }
 

@@ -27,7 +27,9 @@ struct AttnArgs {
   float2* part_ml;      // forward: [splits][nr H] maximum and sum
   const float2* stat;   // gradient: [nr H] log-sum (base 2), delta
   float4* rowpart;      // gradient: [splits][nr H] position and slope sums
-  float4* colpart;      // gradient: [KV][ns] position sums
+  float4* colpart;      // gradient: [kv_splits][KV][ns] position sums
+  int kv_splits;        // parts of the receivers (key and value gradients)
+  float *part_k, *part_v;   // [kv_splits][ns KV][D] partial rows
   void *qb, *kb, *vb;
 };
 
@@ -323,15 +325,18 @@ template <class T, int DP>
 constexpr int kStep = sizeof(T) == 4 && DP > 64 ? 32 : 64;
 
 // How a call runs (fc_attention.cu): on the tcgen05 kernels or the strip
-// kernels, and in how many parts of the senders (forward, query gradient).
+// kernels, and in how many parts of the senders (forward, query gradient) or
+// of the receivers (key and value gradients).
 struct AttnPlan {
-  bool tc;
-  int splits;
+  bool tc, tc_vjp;
+  int splits, q_splits, kv_splits;
 };
 int check_attn(const fc_attn_desc* d, int n_struct, int n_recv, int n_send);
 AttnPlan attn_plan(const fc_attn_desc* d, int n_struct, int n_recv, int n_send);
 int attn_pad(int head_dim);
 // fc_attention_tc.cu: 16-bit types
 int launch_attn_fwd_tc(int dtype, const AttnArgs& a, cudaStream_t s);
+// fc_attention_tc_vjp.cu: 16-bit types, at most 64 heads to a key head
+int launch_attn_vjp_tc(int dtype, bool kv, const AttnArgs& a, cudaStream_t s);
 
 }  // namespace fc

@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
       // Warp cw brings in tiles cw, cw + 3, ..; all three copy the receivers' rows first.
       const int cw = warp - 9;
       const T* q = static_cast<const T*>(a.q);
-      for (int r0 = cw * 4; r0 < kAtRows; r0 += 12) {
+      // (none without a tile to meet: the merge at the end goes over their place)
+      for (int r0 = cw * 4; r0 < kAtRows && nt > 0; r0 += 12) {
         const long long vr = at.v0 + r0 + (lane >> 3);
         const bool ok = vr < at.v1;
         const uint32_t u = (uint32_t)(ok ? vr : at.v0), node = u / (uint32_t)a.G;
@@ -477,12 +478,12 @@ static PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   }
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
-bool at_tensor_map(CUtensorMap* m, bool half, const void* base, int D, int heads, long long ld, int rows) {
+bool at_tensor_map(CUtensorMap* m, bool half, const void* base, int D, int heads, long long ld, int rows, int group) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
-  const cuuint32_t box[3] = {64, 1, kAtStep}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(kAtStep / group)}, es[3] = {1, 1, 1};
   return enc(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -516,18 +517,24 @@ int launch_attn_fwd_tc(int dtype, const AttnArgs& a, cudaStream_t s) {
   return a.o32 ? run_fwd_dim<__half, 2>(a, s) : run_fwd_dim<__half, 1>(a, s);
 }
 
+int attn_vjp_tc_take_error(int* flag, cudaStream_t s);
+int attn_vjp_tc_set_wait(unsigned long long ns);
+
 int attn_tc_take_error(int* flag, cudaStream_t s) {
+  int vjp = 0;
   if (cudaMemcpyFromSymbolAsync(flag, g_at_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
+      cudaStreamSynchronize(s) != cudaSuccess || attn_vjp_tc_take_error(&vjp, s) != FC_OK)
     return FC_ERR_CUDA;
   const int zero = 0;
   if (*flag && (cudaMemcpyToSymbolAsync(g_at_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
                 cudaStreamSynchronize(s) != cudaSuccess))
     return FC_ERR_CUDA;
+  *flag |= vjp;
   return FC_OK;
 }
 int attn_tc_set_wait(unsigned long long ns) {
-  return cudaMemcpyToSymbol(g_at_wait_ns, &ns, sizeof(ns)) == cudaSuccess ? FC_OK : FC_ERR_CUDA;
+  if (cudaMemcpyToSymbol(g_at_wait_ns, &ns, sizeof(ns)) != cudaSuccess) return FC_ERR_CUDA;
+  return attn_vjp_tc_set_wait(ns);
 }
 
 }  // namespace fc

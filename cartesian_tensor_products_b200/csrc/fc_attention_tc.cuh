@@ -131,7 +131,9 @@ __device__ __forceinline__ void load_panel(uint32_t dst, const CUtensorMap* map,
 }
 // [rows][heads][D] of 16-bit values, row step ld, as {D, heads, rows}; the box
 // is one panel.  False if the driver refuses it.
-bool at_tensor_map(CUtensorMap* m, bool half, const void* base, int D, int heads, long long ld, int rows);
+// (`group` heads of 64 / group rows, both counted down where they do not divide).
+bool at_tensor_map(CUtensorMap* m, bool half, const void* base, int D, int heads, long long ld, int rows, int group = 1);
+// error word and wait bound of these kernels (one of each per source file)
 
 // Descriptors (128-byte swizzle) of a tile whose panels have R rows, from byte
 // address a, and their 16-value or 16-row steps.

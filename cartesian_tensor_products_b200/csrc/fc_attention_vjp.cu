@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
   int rlo, rhi;
   other_side(a.recv_ptr, a.B, a.nr, at.b, rlo, rhi);
   const long long r0 = (long long)rlo * a.G, r1 = (long long)rhi * a.G;
-  const long long steps = r1 > r0 ? (r1 - r0 + BN - 1) / BN : 0;
+  const long long all = r1 > r0 ? (r1 - r0 + BN - 1) / BN : 0;
+  const long long t0 = all * blockIdx.z / a.kv_splits, steps = all * (blockIdx.z + 1) / a.kv_splits - t0;
   auto shown = [&](long long j) { return j < at.v1 && (!a.mask || a.mask[j]); };
   auto live = [&](int r) { return shown(at.v0 + r); };
   load_rows<T, DP, 64, 128>(
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
   load_rows<T, DP, 64, 128>(
       vs, a.D, tid, [&](int r) { return static_cast<const T*>(a.v) + (at.v0 + r) * a.ldv + (long long)kvh * a.D; }, live);
   auto load_q = [&](long long t, int st) {
-    const long long b = r0 + t * BN;
+    const long long b = r0 + (t0 + t) * BN;
     auto at_row = [&](const T* base, long long ld, int r) {
       return base + (b + r) / a.G * ld + (kvh * a.G + (b + r) % a.G) * (long long)a.D;
     };
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
     }
     if (vj[h] >= at.v1) continue;
     if (a.colpart && (lane & 3) == 0)
-      a.colpart[(long long)kvh * a.ns + vj[h]] =
+      a.colpart[((long long)blockIdx.z * a.KV + kvh) * a.ns + vj[h]] =
           keep[h] ? make_float4(bx[h], by[h], bz[h], 0.f) : make_float4(0.f, 0.f, 0.f, 0.f);
     const long long row = vj[h] * a.KV + kvh;
     // a hidden sender's row is 0 even where the receivers hold NaN
@@ -332,25 +333,32 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
       if (d * 8 >= a.D) continue;
       const float k2[2] = {keep[h] ? dk[d][2 * h] * a.scale : 0.0f, keep[h] ? dk[d][2 * h + 1] * a.scale : 0.0f};
       const float v2[2] = {keep[h] ? dv[d][2 * h] : 0.0f, keep[h] ? dv[d][2 * h + 1] : 0.0f};
+      if (a.kv_splits > 1) {
+        const long long pr = ((long long)blockIdx.z * a.ns * a.KV + row) * a.D + d * 8 + c2;
+        if (a.kb) store_pack<float, 2>(a.part_k + pr, k2);
+        if (a.vb) store_pack<float, 2>(a.part_v + pr, v2);
+        continue;
+      }
       if (a.kb) store_pack<T, 2>(static_cast<T*>(a.kb) + row * a.D + d * 8 + c2, k2);
       if (a.vb) store_pack<T, 2>(static_cast<T*>(a.vb) + row * a.D + d * 8 + c2, v2);
     }
   }
 }
 
-// Adds the parts of the query gradient.  One warp per row and head.
+// Adds the parts of gradient rows, one warp per row: to[row] = sum of part[s][row].
 template <class T>
-__global__ void __launch_bounds__(256) attn_vjp_join_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(256) attn_vjp_join_kernel(long long rows, int D, int splits,
+                                                            const float* __restrict__ part, T* __restrict__ to) {
   const int c = (threadIdx.x & 31) * 4;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const long long node = row / a.H;
-  if (node >= a.nr || c >= a.D) return;
+  if (row >= rows || c >= D) return;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < a.splits; ++s) {
-    const float4 v = *reinterpret_cast<const float4*>(a.part + ((long long)s * a.nr * a.H + row) * a.D + c);
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(part + (s * rows + row) * D + c);
     acc[0] += v.x; acc[1] += v.y; acc[2] += v.z; acc[3] += v.w;
   }
-  store_pack<T, 4>(static_cast<T*>(a.qb) + row * a.D + c, acc);
+  store_pack<T, 4>(to + row * D + c, acc);
 }
 
 // Position gradients, one warp per node: a receiver's parts and heads, a
@@ -367,7 +375,7 @@ __global__ void __launch_bounds__(256) attn_pos_kernel(AttnArgs a, bool recv, bo
       x += v.x; y += v.y; z += v.z;
     }
   if (send)
-    for (int e = lane; e < a.KV; e += 32) {
+    for (int e = lane; e < a.KV * a.kv_splits; e += 32) {
       const float4 v = a.colpart[(long long)e * a.ns + i];
       x += v.x; y += v.y; z += v.z;
     }
@@ -402,18 +410,23 @@ __global__ void __launch_bounds__(256) attn_slope_kernel(AttnArgs a, float* __re
 // ----------------------------------------------------------------- launches
 
 struct VjpLayout {
-  int splits;
-  size_t stat, part, rowpart, colpart, bytes;
+  AttnPlan plan;
+  size_t stat, part, rowpart, colpart, part_k, part_v, bytes;
 };
 static VjpLayout vjp_layout(const fc_attn_desc* d, int B, int nr, int ns) {
   VjpLayout l;
-  l.splits = attn_plan(d, B, nr, ns).splits;
-  const size_t rows = (size_t)nr * d->heads;
+  l.plan = attn_plan(d, B, nr, ns);
+  const size_t rows = (size_t)nr * d->heads, cols = (size_t)ns * d->kv_heads;
+  const size_t rp = rows * l.plan.q_splits, cp = cols * l.plan.kv_splits;
+  const size_t pq = l.plan.q_splits > 1 ? round16(rp * d->head_dim * sizeof(float)) : 0;
+  const size_t pk = l.plan.kv_splits > 1 ? round16(cp * d->head_dim * sizeof(float)) : 0;
   l.stat = 0;
   l.rowpart = round16(rows * sizeof(float2));
-  l.colpart = l.rowpart + rows * l.splits * sizeof(float4);
-  l.part = l.colpart + (size_t)ns * d->kv_heads * sizeof(float4);
-  l.bytes = l.part + (l.splits > 1 ? round16(rows * l.splits * d->head_dim * sizeof(float)) : 0);
+  l.colpart = l.rowpart + rp * sizeof(float4);
+  l.part = l.colpart + cp * sizeof(float4);
+  l.part_k = l.part + pq;
+  l.part_v = l.part_k + pk;
+  l.bytes = l.part_v + pk;
   return l;
 }
 
@@ -423,36 +436,58 @@ struct VjpWants {
 };
 
 template <class T, int DP>
-static int run_vjp(const AttnArgs& a, const VjpWants& w, const float* o32, float2* stat, cudaStream_t s) {
+static int run_strips(bool kv, const AttnArgs& a, cudaStream_t s) {
   static DeviceFlags ready_q, ready_kv;
   constexpr size_t bytes = VjpSmem<T, DP>::bytes;
-  if (set_smem_once(ready_q, attn_vjp_q_kernel<T, DP>, bytes) != FC_OK ||
-      set_smem_once(ready_kv, attn_vjp_kv_kernel<T, DP>, bytes) != FC_OK)
-    return FC_ERR_CUDA;
-  if (a.nr > 0)
-    attn_stat_kernel<T><<<(unsigned)(((long long)a.nr * a.H + 31) / 32), 256, 0, s>>>(a, o32, a.lse, stat);
-  if (a.nr > 0 && (a.qb || w.pos_recv_bar || w.slope_bar)) {
+  if (kv) {
+    if (set_smem_once(ready_kv, attn_vjp_kv_kernel<T, DP>, bytes) != FC_OK) return FC_ERR_CUDA;
+    attn_vjp_kv_kernel<T, DP>
+        <<<dim3((unsigned)tile_slots(a.B, a.ns, 1, 64), a.KV, a.kv_splits), 128, bytes, s>>>(a);
+  } else {
+    if (set_smem_once(ready_q, attn_vjp_q_kernel<T, DP>, bytes) != FC_OK) return FC_ERR_CUDA;
     attn_vjp_q_kernel<T, DP><<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, 64), a.KV, a.splits), 128, bytes, s>>>(a);
-    if (a.qb && a.splits > 1)
-      attn_vjp_join_kernel<T><<<(unsigned)(((long long)a.nr * a.H + 7) / 8), 256, 0, s>>>(a);
   }
-  if (a.ns > 0 && w.kv)
-    attn_vjp_kv_kernel<T, DP><<<dim3((unsigned)tile_slots(a.B, a.ns, 1, 64), a.KV), 128, bytes, s>>>(a);
-  if (w.pos_recv_bar && a.nr > 0)
-    attn_pos_kernel<<<(unsigned)(((long long)a.nr + 7) / 8), 256, 0, s>>>(a, true, w.self, a.nr, w.pos_recv_bar);
-  if (w.pos_send_bar && a.ns > 0)
-    attn_pos_kernel<<<(unsigned)(((long long)a.ns + 7) / 8), 256, 0, s>>>(a, false, true, a.ns, w.pos_send_bar);
-  if (w.slope_bar) attn_slope_kernel<<<a.H, 256, 0, s>>>(a, w.slope_bar);
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
 }
 
 template <class T>
-static int run_vjp_type(const AttnArgs& a, const VjpWants& w, const float* o32, float2* stat, cudaStream_t s) {
+static int run_side(int dtype, bool tc, bool kv, const AttnArgs& a, cudaStream_t s) {
+  if (tc) return launch_attn_vjp_tc(dtype, kv, a, s);
   switch (attn_pad(a.D)) {
-    case 32: return run_vjp<T, 32>(a, w, o32, stat, s);
-    case 64: return run_vjp<T, 64>(a, w, o32, stat, s);
-    default: return run_vjp<T, 128>(a, w, o32, stat, s);
+    case 32: return run_strips<T, 32>(kv, a, s);
+    case 64: return run_strips<T, 64>(kv, a, s);
+    default: return run_strips<T, 128>(kv, a, s);
   }
+}
+
+template <class T>
+static int run_vjp(int dtype, const AttnArgs& a, const VjpWants& w, bool tc, const float* o32, float2* stat,
+                   cudaStream_t s) {
+  const auto blocks = [](long long rows, int per) { return (unsigned)((rows + per - 1) / per); };
+  const long long rows = (long long)a.nr * a.H, cols = (long long)a.ns * a.KV;
+  int rc = FC_OK;
+  if (a.nr > 0) attn_stat_kernel<T><<<blocks(rows, 32), 256, 0, s>>>(a, o32, a.lse, stat);
+  if (a.nr > 0 && (a.qb || w.pos_recv_bar || w.slope_bar)) {
+    rc = run_side<T>(dtype, tc, false, a, s);
+    if (a.qb && a.splits > 1)
+      attn_vjp_join_kernel<T><<<blocks(rows, 8), 256, 0, s>>>(rows, a.D, a.splits, a.part, static_cast<T*>(a.qb));
+  }
+  if (rc == FC_OK && a.ns > 0 && w.kv) {
+    rc = run_side<T>(dtype, tc, true, a, s);
+    if (a.kv_splits > 1) {
+      if (a.kb)
+        attn_vjp_join_kernel<T><<<blocks(cols, 8), 256, 0, s>>>(cols, a.D, a.kv_splits, a.part_k, static_cast<T*>(a.kb));
+      if (a.vb)
+        attn_vjp_join_kernel<T><<<blocks(cols, 8), 256, 0, s>>>(cols, a.D, a.kv_splits, a.part_v, static_cast<T*>(a.vb));
+    }
+  }
+  if (rc != FC_OK) return rc;
+  if (w.pos_recv_bar && a.nr > 0)
+    attn_pos_kernel<<<blocks(a.nr, 8), 256, 0, s>>>(a, true, w.self, a.nr, w.pos_recv_bar);
+  if (w.pos_send_bar && a.ns > 0)
+    attn_pos_kernel<<<blocks(a.ns, 8), 256, 0, s>>>(a, false, true, a.ns, w.pos_send_bar);
+  if (w.slope_bar) attn_slope_kernel<<<a.H, 256, 0, s>>>(a, w.slope_bar);
+  return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
 }
 
 }  // namespace fc
@@ -516,15 +551,20 @@ int fc_node_attention_vjp(const fc_attn_desc* desc, int n_struct, int n_recv, in
   a.recv_ptr = recv_ptr; a.send_ptr = send_ptr; a.q = q; a.k = k; a.v = v; a.g = g;
   a.pos_r = pos_recv; a.pos_s = pos_send ? pos_send : pos_recv; a.slope = slope; a.mask = send_mask;
   a.lse = const_cast<float*>(lse);
-  a.splits = l.splits;
+  a.splits = l.plan.q_splits;
+  a.kv_splits = l.plan.kv_splits;
+  a.part_k = reinterpret_cast<float*>(ws + l.part_k);
+  a.part_v = reinterpret_cast<float*>(ws + l.part_v);
   a.stat = stat;
   a.rowpart = pos_recv_bar || slope_bar ? reinterpret_cast<float4*>(ws + l.rowpart) : nullptr;
   a.colpart = pos_send_bar || (w.self && pos_recv_bar) ? reinterpret_cast<float4*>(ws + l.colpart) : nullptr;
   a.part = reinterpret_cast<float*>(ws + l.part);
   a.qb = q_bar; a.kb = k_bar; a.vb = v_bar;
-  if (desc->dtype == FC_F32) return run_vjp_type<float>(a, w, out_f32, stat, s);
-  if (desc->dtype == FC_BF16) return run_vjp_type<__nv_bfloat16>(a, w, out_f32, stat, s);
-  return run_vjp_type<__half>(a, w, out_f32, stat, s);
+  // the tensor maps need rows on both sides
+  const bool tc = l.plan.tc_vjp && n_recv > 0 && n_send > 0;
+  if (desc->dtype == FC_F32) return run_vjp<float>(FC_F32, a, w, false, out_f32, stat, s);
+  if (desc->dtype == FC_BF16) return run_vjp<__nv_bfloat16>(FC_BF16, a, w, tc, out_f32, stat, s);
+  return run_vjp<__half>(FC_F16, a, w, tc, out_f32, stat, s);
 }
 
 }  // extern "C"

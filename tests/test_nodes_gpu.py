@@ -269,6 +269,15 @@ ATTN = {
     "many tiles": dict(recv=[1300], send=None, h=16, kv=16, d=32, dtype=BF16, cap=6.0),
     "many tiles wide": dict(recv=[900, 650], send=None, h=16, kv=8, d=128, dtype=F16, hide=0.1),
     "many tiles no bias": dict(recv=[1250], send=None, h=16, kv=16, d=64, dtype=BF16, bias=False),
+    # groups of heads that do not divide a tile of 64 rows, masks, both sides apart
+    "group of 3": dict(recv=[300, 131], send=None, h=6, kv=2, d=64, dtype=BF16, cap=8.0),
+    "group of 5": dict(recv=[260], send=None, h=10, kv=2, d=96, dtype=F16, hide=0.2),
+    "group of 40": dict(recv=[150], send=None, h=40, kv=1, d=48, dtype=BF16, bias=False, cap=5.0),
+    "apart wide": dict(recv=[150, 0, 200], send=[400, 30, 300], h=2, kv=2, d=128, dtype=BF16, cap=9.0, hide=0.3),
+    "few receivers": dict(recv=[130, 100], send=[1900, 900], h=2, kv=2, d=32, dtype=F16),
+    "few senders": dict(recv=[1500, 900], send=[150, 140], h=4, kv=2, d=64, dtype=BF16, cap=9.0),
+    "few senders f32": dict(recv=[1500, 900], send=[50, 70], h=4, kv=2, d=24, dtype=F32),
+    "outside rows bf16": dict(recv=[200, 270], send=None, h=2, kv=2, d=64, dtype=BF16, lead=5, tail=350),
     "many": dict(recv=[(7 * i) % 23 for i in range(300)], send=None, h=2, kv=2, d=16, dtype=F32),
 }
 
