@@ -46,11 +46,13 @@ class LadderDesc(ct.Structure):
 
 
 class HeadDesc(ct.Structure):
+    __hash__ = object.__hash__     # by identity: cached scratch sizes are looked up by it
     _fields_ = [("dtype", ct.c_int), ("heads_q", ct.c_int), ("heads_k", ct.c_int),
                 ("head_dim", ct.c_int), ("pairs", ct.c_int), ("eps", ct.c_float)]
 
 
 class AttnDesc(ct.Structure):
+    __hash__ = object.__hash__
     _fields_ = [("dtype", ct.c_int), ("heads", ct.c_int), ("kv_heads", ct.c_int),
                 ("head_dim", ct.c_int), ("scale", ct.c_float), ("cap", ct.c_float)]
 
@@ -522,68 +524,102 @@ def interaction_block(lmax, order, rowptr, edge_index, edge_vec, x, omega, path_
 
 # ----------------------------------------------------------------------------
 # operators on node rows (include/flashcart_nodes.h)
+#
+# These calls are often a few microseconds of GPU work, so that the checks
+# below are written to cost little: plain integers for pointers and stream,
+# descriptors and scratch sizes looked up by their values.
 
+_F32, _U8, _I32 = torch.float32, torch.uint8, torch.int32
 _ROW_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 def _node_op(f):
     """Runs a node operator on its first tensor's device and on `stream` (None:
-    that device's current stream).  Outputs and scratch are allocated on the
-    stream that uses them."""
+    that device's current stream), which f gets as the raw handle.  Outputs and
+    scratch are allocated on the stream that uses them."""
     @functools.wraps(f)
     def call(first, *args, stream=None, **kw):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError("%s takes CUDA tensors" % f.__name__)
-        dev = first.device
-        if stream is None and dev.index == torch.cuda.current_device():
-            return f(first, *args, stream=torch.cuda.current_stream(), **kw)
-        if stream is not None and stream.device != dev:
-            raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, dev))
-        with torch.cuda.device(dev), torch.cuda.stream(stream):
-            return f(first, *args, stream=torch.cuda.current_stream(), **kw)
+        index = first.get_device()
+        if stream is None and index == torch._C._cuda_getDevice():
+            return f(first, *args, stream=torch._C._cuda_getCurrentRawStream(index), **kw)
+        if stream is not None and stream.device.index != index:
+            raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, first.device))
+        with torch.cuda.device(index), torch.cuda.stream(stream):
+            return f(first, *args, stream=torch._C._cuda_getCurrentRawStream(index), **kw)
     return call
 
 
-def _on(t, dtype, name, like, shape=None):
-    """A contiguous tensor on the device of `like`; None passes."""
+def _on(t, dtype, name, index, shape):
+    """Address of a contiguous tensor on device `index`; None passes as NULL."""
     if t is None:
         return None
-    _dev(t, dtype, name)
-    if t.device != like.device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    return t
-
-
-def _rows(t, name, like=None, shape=None):
-    """Row step of [N][heads][head_dim] rows: the heads of a row are packed,
-    rows may be a column block of a wider array."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype not in _ROW_DTYPES:
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, index))
+    if t.shape != shape:
+        raise ValueError("%s shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _row_dtype(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    d = _ROW_DTYPES.get(t.dtype)
+    if d is None:
         raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
+    return d
+
+
+def _rows(t, name, dtype, index, shape):
+    """(address, row step) of [N][heads][head_dim] rows: the heads of a row are
+    packed, rows may be a column block of a wider array."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, index))
+    if t.shape != shape:
+        raise ValueError("%s shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    n, h, d = shape
+    sn, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
+        raise ValueError("%s: the heads of a row must be packed" % name)
+    return t.data_ptr(), sn if n > 1 else h * d
+
+
+def _rows3(t, name):
     if t.dim() != 3:
         raise ValueError("%s shape %s, expected [nodes][heads][head_dim]" % (name, tuple(t.shape)))
-    if like is not None:
-        if t.device != like.device:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
-        if t.dtype != like.dtype:
-            raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
-        raise ValueError("%s: the heads of a row must be packed" % name)
-    return t.stride(0) if n > 1 else h * d
+    return t.shape
 
 
-def _bytes(workspace, need, like):
-    """Scratch of `need` bytes: a new buffer, or the caller's with its real size."""
-    if workspace is not None and workspace.device != like.device:
-        raise ValueError("workspace is on %s, expected %s" % (workspace.device, like.device))
-    workspace, size = _scratch(workspace, need, like.device)
-    return workspace, size if workspace is not None else 0
+@functools.lru_cache(maxsize=256)
+def _scratch_size(index, query, desc, *sizes):
+    f = getattr(_lib, query)
+    return f(desc, *sizes) if desc is not None else f(*sizes)
+
+
+def _bytes(workspace, need, index):
+    """(tensor, address, size) of scratch: a new buffer of `need` bytes, or the
+    caller's with its real size."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=_U8, device=index)
+        return workspace, workspace.data_ptr(), need
+    if not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if workspace.get_device() != index:
+        raise ValueError("workspace is on %s, expected cuda:%d" % (workspace.device, index))
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 @_node_op
@@ -591,20 +627,16 @@ def species_embed(species, table, lmax=0, scale=1.0, out=None, stream=None):
     """Node features [N][(lmax+1)^2 C] of the species (int32 [N]): scale times
     the table's row [n_species][C] in the rank-0 block, zero elsewhere.  A
     species outside the table (padding: -1) gets a zero row."""
-    _on(species, torch.int32, "species", species)
-    if table.dtype not in _ROW_DTYPES:
-        raise TypeError("table must be float32, bfloat16 or float16, got %s" % table.dtype)
-    _on(table, table.dtype, "table", species)
+    index, dtype = species.get_device(), _row_dtype(table, "table")
     if species.dim() != 1 or table.dim() != 2:
         raise ValueError("species [N] and table [n_species][C] expected")
-    N, (V, C) = species.shape[0], table.shape
+    (N,), (V, C) = species.shape, table.shape
     shape = (N, (lmax + 1) ** 2 * C)
     if out is None:
-        out = torch.empty(shape, dtype=table.dtype, device=table.device)
-    else:
-        _on(out, table.dtype, "out", species, shape)
-    _check(_lib.fc_species_embed(_ROW_DTYPES[table.dtype], N, V, lmax, C, scale, _ptr(species),
-                                 _ptr(table), _ptr(out), _stream(stream)), "fc_species_embed")
+        out = table.new_empty(shape)
+    _check(_lib.fc_species_embed(dtype, N, V, lmax, C, scale, _on(species, _I32, "species", index, (N,)),
+                                 _on(table, table.dtype, "table", index, (V, C)),
+                                 _on(out, table.dtype, "out", index, shape), stream), "fc_species_embed")
     return out
 
 
@@ -612,37 +644,38 @@ def species_embed(species, table, lmax=0, scale=1.0, out=None, stream=None):
 def species_embed_vjp(species, g, n_species, lmax=0, scale=1.0, workspace=None, stream=None):
     """table_bar [n_species][C] (float32) of species_embed for the gradient g
     [N][(lmax+1)^2 C] of its output: the rank-0 rows summed by species."""
-    _on(species, torch.int32, "species", species)
-    if g.dtype not in _ROW_DTYPES:
-        raise TypeError("g must be float32, bfloat16 or float16, got %s" % g.dtype)
-    _on(g, g.dtype, "g", species)
-    N, NY = species.shape[0], (lmax + 1) ** 2
-    if species.dim() != 1 or g.dim() != 2 or g.shape[0] != N or g.shape[1] % NY:
-        raise ValueError("g shape %s" % (tuple(g.shape),))
-    C = g.shape[1] // NY
-    bar = torch.empty((n_species, C), dtype=torch.float32, device=g.device)
-    workspace, size = _bytes(workspace, _lib.fc_species_embed_vjp_workspace_size(N, n_species, C), g)
-    _check(_lib.fc_species_embed_vjp(_ROW_DTYPES[g.dtype], N, n_species, lmax, C, scale,
-                                     _ptr(species), _ptr(g), _ptr(bar), _ptr(workspace), size,
-                                     _stream(stream)), "fc_species_embed_vjp")
+    index, dtype = species.get_device(), _row_dtype(g, "g")
+    NY = (lmax + 1) ** 2
+    if species.dim() != 1 or g.dim() != 2 or g.shape[1] % NY:
+        raise ValueError("species [N] and g [N][(lmax+1)^2 C] expected")
+    N, C = species.shape[0], g.shape[1] // NY
+    bar = torch.empty((n_species, C), dtype=_F32, device=index)
+    need = _scratch_size(index, "fc_species_embed_vjp_workspace_size", None, N, n_species, C)
+    workspace, ws, size = _bytes(workspace, need, index)
+    _check(_lib.fc_species_embed_vjp(dtype, N, n_species, lmax, C, scale,
+                                     _on(species, _I32, "species", index, (N,)),
+                                     _on(g, g.dtype, "g", index, (N, NY * C)), bar.data_ptr(), ws, size,
+                                     stream), "fc_species_embed_vjp")
     return bar
 
 
+@functools.lru_cache(maxsize=256)
+def _head_desc(*fields):
+    return HeadDesc(*fields)
+
+
 def _head_args(x, heads_q, gamma_q, gamma_k, pos, freq, eps):
-    ldx = _rows(x, "x")
-    N, H, D = x.shape
+    index, dtype = x.get_device(), _row_dtype(x, "x")
+    N, H, D = _rows3(x, "x")
+    px, ldx = _rows(x, "x", x.dtype, index, (N, H, D))
     if not 0 <= heads_q <= H:
         raise ValueError("heads_q %d of %d heads" % (heads_q, H))
-    _on(gamma_q, torch.float32, "gamma_q", x, (D,))
-    _on(gamma_k, torch.float32, "gamma_k", x, (D,))
     if (pos is None) != (freq is None):
         raise ValueError("pos and freq go together")
-    R = 0
-    if freq is not None:
-        R = freq.shape[-1]
-        _on(freq, torch.float32, "freq", x, (3, R))
-        _on(pos, torch.float32, "pos", x, (N, 3))
-    return ldx, HeadDesc(_ROW_DTYPES[x.dtype], heads_q, H - heads_q, D, R, eps)
+    R = 0 if freq is None else freq.shape[-1]
+    small = (_on(gamma_q, _F32, "gamma_q", index, (D,)), _on(gamma_k, _F32, "gamma_k", index, (D,)),
+             _on(pos, _F32, "pos", index, (N, 3)), _on(freq, _F32, "freq", index, (3, R)))
+    return index, px, ldx, small, _head_desc(dtype, heads_q, H - heads_q, D, R, eps)
 
 
 @_node_op
@@ -652,12 +685,11 @@ def head_norm_rotate(x, heads_q, gamma_q=None, gamma_k=None, pos=None, freq=None
     queries, the rest keys; x may be a column block of a fused projection) and
     their rotation by theta_f = pos . freq[:, f] of pairs (f, f + R), with pos
     [N][3] and freq [3][R] (None: norm only).  Returns rows like x, packed."""
-    ldx, d = _head_args(x, heads_q, gamma_q, gamma_k, pos, freq, eps)
+    index, px, ldx, small, d = _head_args(x, heads_q, gamma_q, gamma_k, pos, freq, eps)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _check(_lib.fc_head_norm_rotate(ct.byref(d), x.shape[0], _ptr(x), ldx, _ptr(gamma_q),
-                                    _ptr(gamma_k), _ptr(pos), _ptr(freq), _ptr(out),
-                                    _rows(out, "out", x, x.shape), _stream(stream)),
+        out = x.new_empty(x.shape)
+    _check(_lib.fc_head_norm_rotate(d, x.shape[0], px, ldx, *small,
+                                    *_rows(out, "out", x.dtype, index, x.shape), stream),
            "fc_head_norm_rotate")
     return out
 
@@ -668,55 +700,50 @@ def head_norm_rotate_vjp(x, g, heads_q, gamma_q=None, gamma_k=None, pos=None, fr
     """(x_bar, gamma_q_bar, gamma_k_bar, pos_bar) of head_norm_rotate for the
     gradient g of its output; entries not in `want` are None, and pos_bar is
     None without positions."""
-    ldx, d = _head_args(x, heads_q, gamma_q, gamma_k, pos, freq, eps)
+    index, px, ldx, small, d = _head_args(x, heads_q, gamma_q, gamma_k, pos, freq, eps)
     N, H, D = x.shape
-    ldg = _rows(g, "g", x, x.shape)
-    new = lambda shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
-    xb = new(x.shape, x.dtype) if "x" in want else None
-    gqb = new((D,)) if "gamma" in want else None
-    gkb = new((D,)) if "gamma" in want else None
-    pb = new((N, 3)) if "pos" in want and pos is not None else None
-    workspace, size = _bytes(workspace, _lib.fc_head_norm_rotate_vjp_workspace_size(ct.byref(d), N)
-                             if "gamma" in want else 0, x)
-    _check(_lib.fc_head_norm_rotate_vjp(ct.byref(d), N, _ptr(x), ldx, _ptr(g), ldg, _ptr(gamma_q),
-                                        _ptr(gamma_k), _ptr(pos), _ptr(freq), _ptr(xb), H * D,
-                                        _ptr(gqb), _ptr(gkb), _ptr(pb), _ptr(workspace), size,
-                                        _stream(stream)), "fc_head_norm_rotate_vjp")
+    xb = x.new_empty((N, H, D)) if "x" in want else None
+    gb = torch.empty((2, D), dtype=_F32, device=index) if "gamma" in want else None
+    pb = torch.empty((N, 3), dtype=_F32, device=index) if "pos" in want and pos is not None else None
+    need = 0 if gb is None else _scratch_size(index, "fc_head_norm_rotate_vjp_workspace_size", d, N)
+    workspace, ws, size = _bytes(workspace, need, index)
+    gq = None if gb is None else gb.data_ptr()
+    _check(_lib.fc_head_norm_rotate_vjp(
+        d, N, px, ldx, *_rows(g, "g", x.dtype, index, x.shape), *small,
+        None if xb is None else xb.data_ptr(), H * D, gq, None if gb is None else gq + 4 * D,
+        None if pb is None else pb.data_ptr(), ws, size, stream), "fc_head_norm_rotate_vjp")
+    gqb, gkb = (None, None) if gb is None else gb.unbind(0)
     return xb, gqb, gkb, pb
 
 
+@functools.lru_cache(maxsize=256)
+def _attn_desc(*fields):
+    return AttnDesc(*fields)
+
+
 def _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask, scale, cap):
-    """Checked descriptor and the arguments both directions share."""
-    ldq = _rows(q, "q")
-    nr, H, D = q.shape
-    ldk = _rows(k, "k", q)
-    ns, KV = k.shape[:2]
-    if k.shape[2] != D:
-        raise ValueError("k shape %s" % (tuple(k.shape),))
-    ldv = _rows(v, "v", q, k.shape)
-    _on(recv_ptr, torch.int32, "recv_ptr", q)
-    if recv_ptr.dim() != 1 or recv_ptr.numel() < 1:
+    """Device index, checked descriptor, sizes, and the arguments both directions share."""
+    index, dtype = q.get_device(), _row_dtype(q, "q")
+    nr, H, D = _rows3(q, "q")
+    ns, KV, _ = _rows3(k, "k")
+    if recv_ptr.dim() != 1 or recv_ptr.shape[0] < 1:
         raise ValueError("recv_ptr shape %s" % (tuple(recv_ptr.shape),))
     if send_ptr is None:
         if nr != ns:
             raise ValueError("send_ptr is needed where senders are not the receivers")
         send_ptr = recv_ptr
-    _on(send_ptr, torch.int32, "send_ptr", q, recv_ptr.shape)
     if (pos is None) != (slope is None) or (pos is None and pos_send is not None):
         raise ValueError("pos and slope go together, pos_send needs both")
-    _on(pos, torch.float32, "pos", q, (nr, 3))
-    _on(pos_send, torch.float32, "pos_send", q, (ns, 3))
-    _on(slope, torch.float32, "slope", q, (H,))
-    _on(send_mask, torch.uint8, "send_mask", q, (ns,))
     if pos is not None and pos_send is None and nr != ns:
         raise ValueError("pos_send is needed where senders are not the receivers")
-    if scale is None:
-        scale = D ** -0.5
-    d = AttnDesc(_ROW_DTYPES[q.dtype], H, KV, D, scale, cap)
-    sizes = (recv_ptr.shape[0] - 1, nr, ns)
-    args = (_ptr(recv_ptr), _ptr(send_ptr), _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(pos),
-            _ptr(pos_send), _ptr(slope), _ptr(send_mask))
-    return d, sizes, args
+    B1 = recv_ptr.shape[0]
+    args = (_on(recv_ptr, _I32, "recv_ptr", index, (B1,)), _on(send_ptr, _I32, "send_ptr", index, (B1,)),
+            *_rows(q, "q", q.dtype, index, (nr, H, D)), *_rows(k, "k", q.dtype, index, (ns, KV, D)),
+            *_rows(v, "v", q.dtype, index, (ns, KV, D)), _on(pos, _F32, "pos", index, (nr, 3)),
+            _on(pos_send, _F32, "pos_send", index, (ns, 3)), _on(slope, _F32, "slope", index, (H,)),
+            _on(send_mask, _U8, "send_mask", index, (ns,)))
+    d = _attn_desc(dtype, H, KV, D, D ** -0.5 if scale is None else scale, cap)
+    return index, d, (B1 - 1, nr, ns), args
 
 
 @_node_op
@@ -730,18 +757,22 @@ def node_attention(q, k, v, recv_ptr, send_ptr=None, pos=None, pos_send=None, sl
     times the distance of pos and pos_send (None: pos).  send_mask: uint8, 0
     hides a sender.  Rows without senders are 0 with lse -inf.  out_f32, which
     node_attention_vjp needs, is None unless residual (float32: it is out)."""
-    d, sizes, args = _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask, scale, cap)
+    index, d, sizes, args = _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask,
+                                       scale, cap)
     nr, H, D = q.shape
-    out = torch.empty((nr, H, D), dtype=q.dtype, device=q.device)
-    lse = torch.empty((nr, H), dtype=torch.float32, device=q.device)
-    o32 = None
+    out = q.new_empty((nr, H, D))
+    lse = torch.empty((nr, H), dtype=_F32, device=index)
+    o32, p32 = None, None
     if residual:
-        o32 = out if q.dtype == torch.float32 else torch.empty((nr, H, D), dtype=torch.float32,
-                                                               device=q.device)
-    workspace, size = _bytes(workspace, _lib.fc_node_attention_workspace_size(ct.byref(d), *sizes), q)
-    _check(_lib.fc_node_attention(ct.byref(d), *sizes, *args, _ptr(out), H * D, _ptr(lse),
-                                  _ptr(o32) if o32 is not out else None, _ptr(workspace), size,
-                                  _stream(stream)), "fc_node_attention")
+        if q.dtype is _F32:
+            o32 = out
+        else:
+            o32 = torch.empty((nr, H, D), dtype=_F32, device=index)
+            p32 = o32.data_ptr()
+    workspace, ws, size = _bytes(workspace, _scratch_size(index, "fc_node_attention_workspace_size", d, *sizes),
+                                 index)
+    _check(_lib.fc_node_attention(d, *sizes, *args, out.data_ptr(), H * D, lse.data_ptr(), p32, ws, size,
+                                  stream), "fc_node_attention")
     return out, lse, o32
 
 
@@ -754,22 +785,23 @@ def node_attention_vjp(q, k, v, out_f32, lse, g, recv_ptr, send_ptr=None, pos=No
     returned.  Without pos_send, pos_bar holds both roles of a node and
     pos_send_bar is None; entries not in `want`, and without a bias those of
     pos and slope, are None."""
-    d, sizes, args = _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask, scale, cap)
+    index, d, sizes, args = _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask,
+                                       scale, cap)
     if out_f32 is None:
         raise ValueError("out_f32 is needed: node_attention(..., residual=True) returns it")
-    _on(out_f32, torch.float32, "out_f32", q, q.shape)
-    _on(lse, torch.float32, "lse", q, q.shape[:2])
-    ldg = _rows(g, "g", q, q.shape)
-    new = lambda shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=q.device)  # noqa: E731
-    qb = new(q.shape, q.dtype) if "q" in want else None
-    kb = new(k.shape, q.dtype) if "k" in want else None
-    vb = new(v.shape, q.dtype) if "v" in want else None
-    pb = new((q.shape[0], 3)) if "pos" in want and pos is not None else None
-    psb = new((k.shape[0], 3)) if "pos" in want and pos_send is not None else None
-    sb = new((q.shape[1],)) if "slope" in want and slope is not None else None
-    workspace, size = _bytes(workspace, _lib.fc_node_attention_vjp_workspace_size(ct.byref(d), *sizes), q)
-    _check(_lib.fc_node_attention_vjp(ct.byref(d), *sizes, *args, _ptr(out_f32), _ptr(lse), _ptr(g),
-                                      ldg, _ptr(qb), _ptr(kb), _ptr(vb), _ptr(pb), _ptr(psb),
-                                      _ptr(sb), _ptr(workspace), size, _stream(stream)),
-           "fc_node_attention_vjp")
+    shape = q.shape
+    _, nr, ns = sizes
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    qb = q.new_empty(shape) if "q" in want else None
+    kb = q.new_empty(k.shape) if "k" in want else None
+    vb = q.new_empty(k.shape) if "v" in want else None
+    pb = torch.empty((nr, 3), dtype=_F32, device=index) if "pos" in want and pos is not None else None
+    psb = torch.empty((ns, 3), dtype=_F32, device=index) if "pos" in want and pos_send is not None else None
+    sb = torch.empty((shape[1],), dtype=_F32, device=index) if "slope" in want and slope is not None else None
+    workspace, ws, size = _bytes(
+        workspace, _scratch_size(index, "fc_node_attention_vjp_workspace_size", d, *sizes), index)
+    _check(_lib.fc_node_attention_vjp(
+        d, *sizes, *args, _on(out_f32, _F32, "out_f32", index, shape), _on(lse, _F32, "lse", index, shape[:2]),
+        *_rows(g, "g", q.dtype, index, shape), at(qb), at(kb), at(vb), at(pb), at(psb), at(sb), ws, size,
+        stream), "fc_node_attention_vjp")
     return qb, kb, vb, pb, psb, sb
