@@ -84,20 +84,28 @@ __global__ void __launch_bounds__(128) attn_fwd_kernel(AttnArgs a) {
     for (int e = 0; e < 4; ++e) acc[d][e] = 0.0f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
+  const bool idle = at.v0 + warp * 16 >= at.v1;
   for (int t = t0; t < t1; ++t) {
     const int st = (t - t0) & 1;
     if (t + 1 < t1) load_kv(t + 1, st ^ 1);
     cp_commit();
     cp_wait<1>();
     __syncthreads();
+    if (idle) {   // none of the warp's rows is there
+      __syncthreads();
+      continue;
+    }
     const float4* in = info + st * BN;
     float s[NT][4];
-    strip_nt<T, DP, NT>(s, qs + warp * 16 * S, ks + st * BN * S);
+    const long long left = shi - slo - (long long)t * BN;
+    const int nl = left >= BN ? NT : (int)(left + 7) / 8;   // column tiles that are there
+    strip_nt<T, DP, NT>(s, qs + warp * 16 * S, ks + st * BN * S, nl);
     if (a.cap > 0.0f) {
+      strip_tanh<T, NT>(s, mul);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = cap2 * cap_tanh<T>(s[n][e] * mul);
+        for (int e = 0; e < 4; ++e) s[n][e] *= cap2;
     } else {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -114,7 +122,7 @@ __global__ void __launch_bounds__(128) attn_fwd_kernel(AttnArgs a) {
           for (int h = 0; h < 2; ++h) {
             const float dx = px[h] - f.x, dy = py[h] - f.y, dz = pz[h] - f.z;
             const float d2 = dx * dx + dy * dy + dz * dz;
-            s[n][2 * h + c] -= sl[h] * (d2 > 0.0f ? d2 * rsq(d2) : 0.0f);
+            s[n][2 * h + c] -= sl[h] * (d2 * rsq(d2 + kD2Seed));
           }
         }
     }
@@ -148,7 +156,7 @@ __global__ void __launch_bounds__(128) attn_fwd_kernel(AttnArgs a) {
         }
       l[h] = l[h] * alpha[h] + sum;
     }
-    strip_pn<T, DP, NT, Two>(acc, s, vs + st * BN * S, alpha[0], alpha[1]);
+    strip_pn<T, DP, NT, Two>(acc, s, vs + st * BN * S, alpha[0], alpha[1], nl);
     __syncthreads();
   }
   cp_wait<0>();
@@ -231,7 +239,7 @@ int check_attn(const fc_attn_desc* d, int n_struct, int n_recv, int n_send) {
   return FC_OK;
 }
 
-int attn_pad(int head_dim) { return head_dim <= 32 ? 32 : head_dim <= 64 ? 64 : 128; }
+int attn_pad(int head_dim) { return head_dim <= 16 ? 16 : head_dim <= 32 ? 32 : head_dim <= 64 ? 64 : 128; }
 
 // Parts of the streamed side: enough blocks to fill the card, each part at
 // least four product steps of an average structure.
@@ -273,6 +281,7 @@ template <class T>
 static int run_strips(const AttnArgs& a, cudaStream_t s) {
   const bool two = sizeof(T) == 2 && a.o32;
   switch (attn_pad(a.D)) {
+    case 16: return two ? run_attn<T, 16, sizeof(T) == 2>(a, s) : run_attn<T, 16, false>(a, s);
     case 32: return two ? run_attn<T, 32, sizeof(T) == 2>(a, s) : run_attn<T, 32, false>(a, s);
     case 64: return two ? run_attn<T, 64, sizeof(T) == 2>(a, s) : run_attn<T, 64, false>(a, s);
     default: return two ? run_attn<T, 128, sizeof(T) == 2>(a, s) : run_attn<T, 128, false>(a, s);

@@ -62,6 +62,54 @@ __device__ __forceinline__ float cap_tanh(float x) {
     return 1.0f - 2.0f * rcp(1.0f + ex2(2.0f * kLog2e * x));
 }
 
+// Squared distances carry 1e-36 where they are inverted, so that a coincident
+// pair has a finite inverse (its distance is then 0, its direction 0).
+constexpr float kD2Seed = 1e-36f;
+
+// tanh of scores over the cap for |x| <= 0.8 as x P(x^2): degree 5, least
+// largest relative error (fitted to tanh(x)/x), 5.8e-8, about one FP32 rounding.
+constexpr float kTanhMax = 0.8f;
+__host__ __device__ constexpr float tanh_c(int i) {
+  return i == 0   ? 0.9999999403953552f
+         : i == 1 ? -0.3333267569541931f
+         : i == 2 ? 0.13321048021316528f
+         : i == 3 ? -0.05311431363224983f
+         : i == 4 ? 0.01909329928457737f
+                  : -0.004355299286544323f;
+}
+__device__ __forceinline__ float tanh_poly(float x) {
+  const float z = x * x;
+  float p = tanh_c(5);
+#pragma unroll
+  for (int i = 4; i >= 0; --i) p = fmaf(z, p, tanh_c(i));
+  return x * p;
+}
+// s = tanh(s mul) of a strip.  Scores are a fraction of the cap nearly always:
+// the polynomial then spares the special-function unit; a warp that holds a
+// larger one takes cap_tanh.
+template <class T, int NT>
+__device__ __forceinline__ void strip_tanh(float (&s)[NT][4], float mul) {
+  float m = 0.0f;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s[n][e] *= mul;
+      m = fmaxf(m, fabsf(s[n][e]));
+    }
+  if (__any_sync(0xffffffffu, !(m <= kTanhMax))) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = cap_tanh<T>(s[n][e]);
+  } else {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = tanh_poly(s[n][e]);
+  }
+}
+
 // Tile t of the rows of all structures, `mult` virtual rows per row and `tile`
 // virtual rows per tile.  The rows before the first structure and after the
 // last count as two more structures (0 and B + 1), which have nothing on the
@@ -189,10 +237,14 @@ __device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint
 // Accumulator fragment of a 16 x 8 NT strip: element e of tile n is row
 // lane/4 + 8 (e/2), column 8 n + 2 (lane%4) + e%2.
 
-// s = A B^T over DP: 16 rows at a, 8 NT rows at b, both in shared tiles.
-// FP32 rows as three TF32 products (hi lo, lo hi, hi hi): error near 2^-21.
+// s = A B^T over DP: 16 rows at a, 8 NT rows at b, both in shared tiles; column
+// tiles from nl on are not there and stay 0.  FP32 rows as three TF32 products
+// (hi lo, lo hi, hi hi), error near 2^-21.  The tensor core truncates every
+// step of its sum (measured: steps below one unit in the last place add
+// nothing), so the FP32 sums are taken out every 32 values and added in FP32,
+// the small products in a sum of their own.
 template <class T, int DP, int NT>
-__device__ __forceinline__ void strip_nt(float (&s)[NT][4], const T* a, const T* b) {
+__device__ __forceinline__ void strip_nt(float (&s)[NT][4], const T* a, const T* b, int nl) {
   constexpr int S = kStride<T, DP>;
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -208,6 +260,7 @@ __device__ __forceinline__ void strip_nt(float (&s)[NT][4], const T* a, const T*
       ldsm4(fa, pa + k);
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
+        if (n >= nl) break;
         uint32_t fb[4];
         ldsm4(fb, pb + n * 8 * S + k);
         mma16<T>(s[n], fa, fb[0], fb[1]);
@@ -218,35 +271,47 @@ __device__ __forceinline__ void strip_nt(float (&s)[NT][4], const T* a, const T*
     const int g = lane >> 2, t = lane & 3;
     const float* pa = a + g * S + t;
     const float* pb = b + g * S + t;
-#pragma unroll 2
-    for (int k = 0; k < DP; k += 8) {
-      uint32_t hi[4], lo[4];
-      tc::split_tf32(pa[k], hi[0], lo[0]);
-      tc::split_tf32(pa[k + 8 * S], hi[1], lo[1]);
-      tc::split_tf32(pa[k + 4], hi[2], lo[2]);
-      tc::split_tf32(pa[k + 8 * S + 4], hi[3], lo[3]);
+    constexpr int KC = DP < 32 ? DP : 32;
+#pragma unroll 1
+    for (int k0 = 0; k0 < DP; k0 += KC) {
+      uint32_t hi[KC / 8][4], lo[KC / 8][4];
+#pragma unroll
+      for (int k = 0; k < KC / 8; ++k) {
+        const float* p = pa + k0 + 8 * k;
+        tc::split_tf32(p[0], hi[k][0], lo[k][0]);
+        tc::split_tf32(p[8 * S], hi[k][1], lo[k][1]);
+        tc::split_tf32(p[4], hi[k][2], lo[k][2]);
+        tc::split_tf32(p[8 * S + 4], hi[k][3], lo[k][3]);
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        uint32_t h0, l0, h1, l1;
-        tc::split_tf32(pb[n * 8 * S + k], h0, l0);
-        tc::split_tf32(pb[n * 8 * S + k + 4], h1, l1);
-        mma8(s[n], hi, l0, l1);
-        mma8(s[n], lo, h0, h1);
-        mma8(s[n], hi, h0, h1);
+        if (n >= nl) break;
+        float big[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KC / 8; ++k) {
+          uint32_t h0, l0, h1, l1;
+          tc::split_tf32(pb[n * 8 * S + k0 + 8 * k], h0, l0);
+          tc::split_tf32(pb[n * 8 * S + k0 + 8 * k + 4], h1, l1);
+          mma8(small, hi[k], l0, l1);
+          mma8(big, hi[k], h0, h1);
+          mma8(small, lo[k], h0, h1);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] += big[e] + small[e];
       }
     }
   }
 }
 
-// acc = alpha acc + P B: P the 16 x 8 NT strip, B 8 NT rows of a shared tile.
-// Each call sums into a fresh fragment that is added to acc in FP32: the
-// tensor core's own accumulation truncates, which over thousands of rows would
-// show in FP32 results.  Two: 16-bit P as two terms (its rounding error and
-// that again), else one rounding to 16 bits, half a unit of 2^-8 (BF16) or
-// 2^-11 (FP16) per weight, which averages over the row.
+// acc = alpha acc + P B: P the 16 x 8 NT strip, B 8 NT rows of a shared tile, of
+// which the column tiles (rows) from nl on are not there.  Each call sums into
+// a fresh fragment that is added to acc in FP32, for the same reason.  Two:
+// 16-bit P as two terms (its rounding error and that again), else one rounding
+// to 16 bits, half a unit of 2^-8 (BF16) or 2^-11 (FP16) per weight, which
+// averages over the row.
 template <class T, int DP, int NT, bool Two>
 __device__ __forceinline__ void strip_pn(float (&acc)[DP / 8][4], const float (&p)[NT][4], const T* b, float alpha0,
-                                         float alpha1) {
+                                         float alpha1, int nl) {
   constexpr int S = kStride<T, DP>;
   const int lane = threadIdx.x & 31;
   if constexpr (sizeof(T) == 2) {
@@ -266,6 +331,7 @@ __device__ __forceinline__ void strip_pn(float (&acc)[DP / 8][4], const float (&
       float f0[4] = {0.f, 0.f, 0.f, 0.f}, f1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
+        if (n >= nl) break;
         uint32_t fb[4];
         ldsm4t(fb, pb + n * 8 * S + d * 8);
         if constexpr (Two) {
@@ -285,36 +351,37 @@ __device__ __forceinline__ void strip_pn(float (&acc)[DP / 8][4], const float (&
     // k slot t of the product is row 2t, slot t + 4 row 2t + 1: the layout that P already has
     const int g = lane >> 2, t = lane & 3;
     const float* pb = b + 2 * t * S + g;
+    constexpr int DC = DP / 8 < 4 ? DP / 8 : 4;
 #pragma unroll
-    for (int d = 0; d < DP / 8; d += 4) {
-      float f[4][4];
+    for (int d = 0; d < DP / 8; d += DC) {
+      float f[DC][4], fs[DC][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < DC; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[i][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) f[i][e] = fs[i][e] = 0.0f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
+        if (n >= nl) break;
         uint32_t hi[4], lo[4];
         tc::split_tf32(p[n][0], hi[0], lo[0]);
         tc::split_tf32(p[n][2], hi[1], lo[1]);
         tc::split_tf32(p[n][1], hi[2], lo[2]);
         tc::split_tf32(p[n][3], hi[3], lo[3]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (d + i >= DP / 8) continue;
+        for (int i = 0; i < DC; ++i) {
           uint32_t h0, l0, h1, l1;
           tc::split_tf32(pb[n * 8 * S + (d + i) * 8], h0, l0);
           tc::split_tf32(pb[(n * 8 + 1) * S + (d + i) * 8], h1, l1);
-          mma8(f[i], hi, l0, l1);
-          mma8(f[i], lo, h0, h1);
+          mma8(fs[i], hi, l0, l1);
           mma8(f[i], hi, h0, h1);
+          mma8(fs[i], lo, h0, h1);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (d + i < DP / 8)
+      for (int i = 0; i < DC; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[d + i][e] = fmaf(acc[d + i][e], e < 2 ? alpha0 : alpha1, f[i][e]);
+        for (int e = 0; e < 4; ++e)
+          acc[d + i][e] = fmaf(acc[d + i][e], e < 2 ? alpha0 : alpha1, f[i][e] + fs[i][e]);
     }
   }
 }

@@ -177,16 +177,12 @@ __device__ __forceinline__ float max_pairs(const float2 (&x)[N]) {
   return max3(fmaxf(m[0], m[1]), m[2], m[3]);
 }
 
-// tanh(x) / x for |x| <= 0.8 as P(x^2), times f: degree 5, least largest
-// relative error (fitted to tanh(x)/x), 5.8e-8, about one FP32 rounding.
-constexpr float kTanhMax = 0.8f;
+// tanh(x) / x for |x| <= 0.8, times f, for pairs (tanh_poly).
 struct TanhPoly {
   float2 c[6];
   __device__ __forceinline__ explicit TanhPoly(float f) {
-    const float k[6] = {0.9999999403953552f, -0.3333267569541931f, 0.13321048021316528f,
-                        -0.05311431363224983f, 0.01909329928457737f, -0.004355299286544323f};
 #pragma unroll
-    for (int i = 0; i < 6; ++i) c[i] = pair(f * k[i]);
+    for (int i = 0; i < 6; ++i) c[i] = pair(f * tanh_c(i));
   }
   __device__ __forceinline__ float2 operator()(float2 z) const {
     float2 p = fma2(z, c[5], c[4]);
@@ -206,9 +202,5 @@ __device__ __forceinline__ bool tanh_in_range(const float2 (&x)[N]) {
   for (int i = 0; i < N; ++i) m[i & 3] = max3_abs(m[i & 3], x[i].x, x[i].y);
   return !__any_sync(0xffffffffu, !(max3(fmaxf(m[0], m[1]), m[2], m[3]) <= kTanhMax));
 }
-
-// Squared distances carry 1e-36 so that a coincident pair has a finite inverse
-// (its distance is then 1e-18, its direction 0).
-constexpr float kD2Seed = 1e-36f;
 
 }  // namespace fc

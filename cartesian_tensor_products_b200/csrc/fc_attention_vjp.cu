@@ -39,19 +39,6 @@ __global__ void __launch_bounds__(256) attn_stat_kernel(AttnArgs a, const float*
   }
 }
 
-// Score in base 2 and the derivative of the cap, from the raw product.
-template <class T>
-__device__ __forceinline__ void capped(const AttnArgs& a, float raw, float mul, float cap2, float& t, float& dc) {
-  if (a.cap > 0.0f) {
-    const float th = cap_tanh<T>(raw * mul);
-    t = cap2 * th;
-    dc = 1.0f - th * th;
-  } else {
-    t = raw * mul;
-    dc = 1.0f;
-  }
-}
-
 template <class T, int DP>
 struct VjpSmem {
   static constexpr int BN = kStep<T, DP> == 64 && DP > 64 ? 32 : kStep<T, DP>;   // streamed rows
@@ -128,34 +115,44 @@ __global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[d][e] = 0.0f;
 
+  const bool idle = at.v0 + warp * 16 >= at.v1;
   for (int t = t0; t < t1; ++t) {
     const int st = (t - t0) & 1;
     if (t + 1 < t1) load_kv(t + 1, st ^ 1);
     cp_commit();
     cp_wait<1>();
     __syncthreads();
+    if (idle) {   // none of the warp's rows is there
+      __syncthreads();
+      continue;
+    }
     const float4* in = info + st * BN;
+    const long long left = shi - slo - (long long)t * BN;
+    const int nl = left >= BN ? NT : (int)(left + 7) / 8;   // column tiles that are there
     float s[NT][4], dp[NT][4];
-    strip_nt<T, DP, NT>(s, qs + warp * 16 * S, ks + st * BN * S);
-    strip_nt<T, DP, NT>(dp, gs + warp * 16 * S, vs + st * BN * S);
+    strip_nt<T, DP, NT>(s, qs + warp * 16 * S, ks + st * BN * S, nl);
+    strip_nt<T, DP, NT>(dp, gs + warp * 16 * S, vs + st * BN * S, nl);
+    if (a.cap > 0.0f) strip_tanh<T, NT>(s, mul);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      if (n >= nl) break;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float4 f = in[n * 8 + c2 + c];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float tt, dc;
-          capped<T>(a, s[n][2 * h + c], mul, cap2, tt, dc);
+          const float th = s[n][2 * h + c];
+          float tt = fmaf(th, a.cap > 0.0f ? cap2 : mul, -lse2[h]);
+          const float dc = a.cap > 0.0f ? fmaf(-th, th, 1.0f) : 1.0f;
           float dx = 0.f, dy = 0.f, dz = 0.f, inv = 0.f, dist = 0.f;
           if (a.pos_r) {
             dx = px[h] - f.x; dy = py[h] - f.y; dz = pz[h] - f.z;
             const float d2 = dx * dx + dy * dy + dz * dz;
-            inv = d2 > 0.0f ? rsq(d2) : 0.0f;
+            inv = rsq(d2 + kD2Seed);
             dist = d2 * inv;
             tt -= sl[h] * kLog2e * dist;
           }
-          const float p = ex2(tt - lse2[h]);
+          const float p = ex2(tt);
           const float dt = f.w != 0.0f ? 0.0f : p * (dp[n][2 * h + c] - delta[h]);
           if (a.pos_r) {
             const float w = dt * inv;
@@ -165,7 +162,8 @@ __global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
           s[n][2 * h + c] = dt * dc;
         }
       }
-    strip_pn<T, DP, NT, false>(acc, s, ks + st * BN * S, 1.0f, 1.0f);
+    }
+    strip_pn<T, DP, NT, false>(acc, s, ks + st * BN * S, 1.0f, 1.0f, nl);
     __syncthreads();
   }
   cp_wait<0>();
@@ -271,34 +269,44 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) dk[d][e] = dv[d][e] = 0.0f;
 
+  const bool idle = at.v0 + warp * 16 >= at.v1;
   for (long long t = 0; t < steps; ++t) {
     const int st = (int)(t & 1);
     if (t + 1 < steps) load_q(t + 1, st ^ 1);
     cp_commit();
     cp_wait<1>();
     __syncthreads();
+    if (idle) {   // none of the warp's senders is there
+      __syncthreads();
+      continue;
+    }
     const float4 *rp = rpos + st * BN, *rs = rst + st * BN;
+    const long long left = r1 - r0 - (t0 + t) * BN;
+    const int nl = left >= BN ? NT : (int)(left + 7) / 8;   // column tiles that are there
     float s[NT][4], dp[NT][4];
-    strip_nt<T, DP, NT>(s, ks + warp * 16 * S, qs + st * BN * S);
-    strip_nt<T, DP, NT>(dp, vs + warp * 16 * S, gs + st * BN * S);
+    strip_nt<T, DP, NT>(s, ks + warp * 16 * S, qs + st * BN * S, nl);
+    strip_nt<T, DP, NT>(dp, vs + warp * 16 * S, gs + st * BN * S, nl);
+    if (a.cap > 0.0f) strip_tanh<T, NT>(s, mul);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      if (n >= nl) break;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float4 f = rp[n * 8 + c2 + c];
         const float2 ld = *reinterpret_cast<const float2*>(&rs[n * 8 + c2 + c]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float tt, dc;
-          capped<T>(a, s[n][2 * h + c], mul, cap2, tt, dc);
+          const float th = s[n][2 * h + c];
+          float tt = fmaf(th, a.cap > 0.0f ? cap2 : mul, -ld.x);
+          const float dc = a.cap > 0.0f ? fmaf(-th, th, 1.0f) : 1.0f;
           float dx = 0.f, dy = 0.f, dz = 0.f, inv = 0.f;
           if (a.pos_r) {
             dx = f.x - px[h]; dy = f.y - py[h]; dz = f.z - pz[h];
             const float d2 = dx * dx + dy * dy + dz * dz;
-            inv = d2 > 0.0f ? rsq(d2) : 0.0f;
+            inv = rsq(d2 + kD2Seed);
             tt -= f.w * kLog2e * (d2 * inv);
           }
-          const float p = keep[h] ? ex2(tt - ld.x) : 0.0f;
+          const float p = keep[h] ? ex2(tt) : 0.0f;
           const float dt = keep[h] ? p * (dp[n][2 * h + c] - ld.y) : 0.0f;
           if (a.pos_r) {
             const float w = dt * f.w * inv;
@@ -308,8 +316,9 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
           dp[n][2 * h + c] = dt * dc;
         }
       }
-    strip_pn<T, DP, NT, false>(dv, s, gs + st * BN * S, 1.0f, 1.0f);
-    strip_pn<T, DP, NT, false>(dk, dp, qs + st * BN * S, 1.0f, 1.0f);
+    }
+    strip_pn<T, DP, NT, false>(dv, s, gs + st * BN * S, 1.0f, 1.0f, nl);
+    strip_pn<T, DP, NT, false>(dk, dp, qs + st * BN * S, 1.0f, 1.0f, nl);
     __syncthreads();
   }
   cp_wait<0>();
@@ -454,6 +463,7 @@ template <class T>
 static int run_side(int dtype, bool tc, bool kv, const AttnArgs& a, cudaStream_t s) {
   if (tc) return launch_attn_vjp_tc(dtype, kv, a, s);
   switch (attn_pad(a.D)) {
+    case 16: return run_strips<T, 16>(kv, a, s);
     case 32: return run_strips<T, 32>(kv, a, s);
     case 64: return run_strips<T, 64>(kv, a, s);
     default: return run_strips<T, 128>(kv, a, s);
