@@ -1,14 +1,16 @@
 // RMS norm of query and key heads with the rotation by node positions, and
 // its VJP, one pass over the rows each.
 //
-// Bound by the rows read and written.  A head is spread over a group of 1 to
-// 32 lanes; a lane holds units of W values f .. f+W-1 together with their
-// rotation partners f+R .. f+R+W-1, so that both 16-byte loads of a pair stay
-// in one lane and the rotation needs no exchange.  W is the widest vector
-// that R is a multiple of (any R is valid: odd ones take scalar units).  The
-// angles of a block's nodes are formed once for all heads, in FP64 reduced to
-// half turns, since FP32 would lose the phase of positions far from the
-// origin.
+// Bound by the rows read and written.  A group of 1 to 32 lanes takes every
+// hs-th head of a node, so that a warp reads one stretch of a row and the node's
+// angles stay in registers over the group's heads (a block forms them once, in
+// shared memory; one group per node instead read 64-byte pieces of eight rows
+// at a time: 98 against 75 us at 65,536 nodes of 16 + 4 BF16 heads of 64).  A lane
+// holds units of W values f .. f+W-1 together with their rotation partners
+// f+R .. f+R+W-1: both loads of a pair are its own and the rotation needs no
+// exchange.  W is the widest vector that R is a multiple of (any R is valid:
+// odd ones take scalar units).  Angles are formed in FP64 and reduced to half
+// turns, since FP32 would lose the phase of positions far from the origin.
 #include <math.h>
 
 #include "fc_nodes.cuh"
@@ -16,7 +18,7 @@
 namespace fc {
 
 struct HeadArgs {
-  int n, hq, hk, d, R, units, lg, tn;   // lg: log2 of the lanes per head; tn: nodes per block step
+  int n, hq, hk, d, R, units, lg, hs;   // lg: log2 of the lanes of a group; hs: groups that share a node's heads
   float eps;
   long long ldx, ldy, ldg, ldxb;
   const float *gq, *gk, *pos, *freq;
@@ -24,9 +26,8 @@ struct HeadArgs {
 };
 
 // cos and sin of angle f of a node
-__device__ __forceinline__ float2 node_angle(const HeadArgs& a, long long node, int f) {
-  const double th = (double)a.pos[3 * node] * a.freq[f] + (double)a.pos[3 * node + 1] * a.freq[a.R + f] +
-                    (double)a.pos[3 * node + 2] * a.freq[2 * a.R + f];
+__device__ __forceinline__ float2 node_angle(const HeadArgs& a, const double (&p)[3], int f) {
+  const double th = p[0] * a.freq[f] + p[1] * a.freq[a.R + f] + p[2] * a.freq[2 * a.R + f];
   const double t = th * 0.31830988618379067154;   // half turns
   float s, c;
   sincospif((float)(t - 2.0 * rint(0.5 * t)), &s, &c);
@@ -40,70 +41,131 @@ __device__ __forceinline__ int unit_at(const HeadArgs& a, int u) {
   return u < p ? u * W : 2 * a.R + (u - p) * W;
 }
 
-template <class T, int W, int NIT>
-__global__ void __launch_bounds__(256) head_norm_kernel(HeadArgs a, const T* __restrict__ x, T* __restrict__ y) {
-  extern __shared__ float sm[];
-  float* gam = sm;                                                 // [2][d]
-  float2* turn = reinterpret_cast<float2*>(sm + 2 * a.d);          // [tn][R]
-  const int tid = threadIdx.x, H = a.hq + a.hk, G = 1 << a.lg;
-  const long long n0 = (long long)blockIdx.x * a.tn;
-  const int here = (int)(a.n - n0 < a.tn ? a.n - n0 : a.tn);
-  for (int i = tid; i < 2 * a.d; i += 256) {
-    const float* g = i < a.d ? a.gq : a.gk;
-    gam[i] = g ? g[i < a.d ? i : i - a.d] : 1.0f;
-  }
-  for (int i = tid; i < here * a.R; i += 256) {
-    const int t = i / a.R;
-    turn[i] = node_angle(a, n0 + t, i - t * a.R);
-  }
-  __syncthreads();
-  const int lane = tid & (G - 1), group = tid >> a.lg, groups = 256 >> a.lg;
-  const int items = here * H;
-  const int first = (tid & ~31) >> a.lg;   // the warp's first group: loop bounds are per warp
-  for (int base = first; base < items; base += groups) {
-    const int it = base + (group - first);
-    const bool live = it < items;
-    const int t = live ? it / H : 0, h = live ? it - t * H : 0;
-    const T* row = x + (n0 + t) * a.ldx + (long long)h * a.d;
-    float p[NIT][W], q[NIT][W], ss = 0.0f;
+// What a lane keeps of a node: its units' places and angles.
+template <int W, int NIT>
+struct LaneUnits {
+  int at[NIT];          // -1: no unit
+  bool pair[NIT];
+  float2 cs[NIT][W];
+
+  __device__ __forceinline__ LaneUnits(const HeadArgs& a, int lane) {
 #pragma unroll
     for (int j = 0; j < NIT; ++j) {
-      const int u = lane + j * G;
+      const int u = lane + (j << a.lg);
+      at[j] = u < a.units ? unit_at<W>(a, u) : -1;
+      pair[j] = at[j] >= 0 && at[j] < a.R;
 #pragma unroll
-      for (int i = 0; i < W; ++i) p[j][i] = q[j][i] = 0.0f;
-      if (live && u < a.units) {
-        const int at = unit_at<W>(a, u);
-        load_pack<T, W>(row + at, p[j]);
-        if (at < a.R) load_pack<T, W>(row + at + a.R, q[j]);
-      }
+      for (int i = 0; i < W; ++i) cs[j][i] = make_float2(1.0f, 0.0f);
+    }
+  }
+  // angles of a node from the block's table
+  __device__ __forceinline__ void node(const float2* turn) {
+#pragma unroll
+    for (int j = 0; j < NIT; ++j)
+      if (pair[j])
+#pragma unroll
+        for (int i = 0; i < W; ++i) cs[j][i] = turn[at[j] + i];
+  }
+  // a head's values as they are stored, zeros where the lane has none
+  template <class T>
+  __device__ __forceinline__ void fetch(const T* row, int R, bool live, Pack<T, W> (&p)[NIT], Pack<T, W> (&q)[NIT]) const {
+#pragma unroll
+    for (int j = 0; j < NIT; ++j) {
+      p[j].clear();
+      q[j].clear();
+      if (live && at[j] >= 0) p[j] = *reinterpret_cast<const Pack<T, W>*>(row + at[j]);
+      if (live && pair[j]) q[j] = *reinterpret_cast<const Pack<T, W>*>(row + at[j] + R);
+    }
+  }
+  // to FP32; the sum of squares
+  template <class T>
+  __device__ __forceinline__ float widen(const Pack<T, W> (&a)[NIT], const Pack<T, W> (&b)[NIT], float (&p)[NIT][W],
+                                         float (&q)[NIT][W]) const {
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NIT; ++j) {
+      a[j].get(p[j]);
+      b[j].get(q[j]);
 #pragma unroll
       for (int i = 0; i < W; ++i) ss += p[j][i] * p[j][i] + q[j][i] * q[j][i];
     }
-    for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    return ss;
+  }
+};
+
+__device__ __forceinline__ float group_sum(float v, int lg) {
+  for (int o = (1 << lg) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// the weights of both kinds, [2][d], and the angles of a block's nodes from n0 on, [nodes][R]
+__device__ __forceinline__ void load_weights(const HeadArgs& a, float* gam) {
+  for (int i = threadIdx.x; i < 2 * a.d; i += 256) {
+    const float* g = i < a.d ? a.gq : a.gk;
+    gam[i] = g ? g[i < a.d ? i : i - a.d] : 1.0f;
+  }
+}
+__device__ __forceinline__ void load_angles(const HeadArgs& a, long long n0, int nodes, float2* turn) {
+  for (int i = threadIdx.x; i < nodes * a.R; i += 256) {
+    const int t = i / a.R;
+    const long long n = n0 + t;
+    if (n >= a.n) break;
+    const double p[3] = {a.pos[3 * n], a.pos[3 * n + 1], a.pos[3 * n + 2]};
+    turn[i] = node_angle(a, p, i - t * a.R);
+  }
+}
+
+template <class T, int W, int NIT>
+__global__ void __launch_bounds__(256) head_norm_kernel(HeadArgs a, const T* __restrict__ x, T* __restrict__ y) {
+  extern __shared__ float sm[];
+  float* gam = sm;
+  float2* turn = reinterpret_cast<float2*>(sm + 2 * a.d);
+  const int lane = threadIdx.x & ((1 << a.lg) - 1), group = threadIdx.x >> a.lg, nodes = (256 >> a.lg) / a.hs;
+  const long long n0 = (long long)blockIdx.x * nodes;
+  const int t = group / a.hs, part = group - t * a.hs, H = a.hq + a.hk;
+  const long long node = n0 + t;
+  const bool there = node < a.n;
+  LaneUnits<W, NIT> u(a, lane);
+  // a head's loads run beside the work on the one before (the first's beside the angles)
+  Pack<T, W> rp[NIT], rq[NIT];
+  auto fetch = [&](int h) {
+    const bool live = there && h < H;
+    u.fetch(x + (live ? node * a.ldx + (long long)h * a.d : 0), a.R, live, rp, rq);
+  };
+  fetch(part);
+  load_weights(a, gam);
+  load_angles(a, n0, nodes, turn);
+  __syncthreads();
+  if (there) u.node(turn + t * a.R);
+  for (int hb = 0; hb < H; hb += a.hs) {   // the same count in every lane
+    const int h = hb + part;
+    const bool live = there && h < H;
+    const long long hd = (long long)h * a.d;
+    float p[NIT][W], q[NIT][W];
+    const float ss = group_sum(u.widen(rp, rq, p, q), a.lg);
+    fetch(h + a.hs);
     const float r = rsqrtf(ss / (float)a.d + a.eps);
     if (!live) continue;
     const float* gm = gam + (h < a.hq ? 0 : a.d);
-    T* out = y + (n0 + t) * a.ldy + (long long)h * a.d;
+    T* out = y + node * a.ldy + hd;
 #pragma unroll
     for (int j = 0; j < NIT; ++j) {
-      const int u = lane + j * G;
-      if (u >= a.units) continue;
-      const int at = unit_at<W>(a, u);
-      float v[W], w[W];
-      if (at < a.R) {
+      if (u.at[j] < 0) continue;
+      float v[W], w[W], ga[W], gb[W];
+      load_pack<float, W>(gm + u.at[j], ga);
+      if (u.pair[j]) {
+        load_pack<float, W>(gm + u.at[j] + a.R, gb);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const float2 cs = turn[t * a.R + at + i];
-          const float ua = p[j][i] * r * gm[at + i], ub = q[j][i] * r * gm[at + a.R + i];
-          v[i] = ua * cs.x - ub * cs.y;
-          w[i] = ua * cs.y + ub * cs.x;
+          const float ua = p[j][i] * r * ga[i], ub = q[j][i] * r * gb[i];
+          v[i] = ua * u.cs[j][i].x - ub * u.cs[j][i].y;
+          w[i] = ua * u.cs[j][i].y + ub * u.cs[j][i].x;
         }
-        store_pack<T, W>(out + at + a.R, w);
+        store_pack<T, W>(out + u.at[j] + a.R, w);
       } else {
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = p[j][i] * r * gm[at + i];
+        for (int i = 0; i < W; ++i) v[i] = p[j][i] * r * ga[i];
       }
-      store_pack<T, W>(out + at, v);
+      store_pack<T, W>(out + u.at[j], v);
     }
   }
 }
@@ -111,171 +173,151 @@ __global__ void __launch_bounds__(256) head_norm_kernel(HeadArgs a, const T* __r
 // The VJP: x, g read once, x_bar written once.  With u = x r gamma and ub the
 // gradient turned back, x_bar = r (gamma ub - xn mean(gamma ub xn)), xn = x r.
 // The gamma gradient stays in registers over all the nodes of a block and is
-// added over blocks by head_gamma_kernel; the position gradient of a node is
-// summed over its heads in shared memory.
+// added over blocks by head_gamma_kernel; the angle gradients of a node stay
+// there over the group's heads.
 template <class T, int W, int NIT>
-__global__ void __launch_bounds__(256) head_norm_vjp_kernel(HeadArgs a, const T* __restrict__ x,
-                                                            const T* __restrict__ g, T* __restrict__ xb) {
+__global__ void __launch_bounds__(256, 2) head_norm_vjp_kernel(HeadArgs a, const T* __restrict__ x,
+                                                               const T* __restrict__ g, T* __restrict__ xb) {
   extern __shared__ float sm[];
-  const int tid = threadIdx.x, H = a.hq + a.hk, G = 1 << a.lg;
-  float* gam = sm;                                                 // [2][d]
-  float* fr = gam + 2 * a.d;                                       // [3][R], padded to 4 R
-  float2* turn = reinterpret_cast<float2*>(fr + 4 * a.R);          // [tn][R]
-  float* pacc = reinterpret_cast<float*>(turn + a.tn * a.R);       // [tn H][3]
-  for (int i = tid; i < 2 * a.d; i += 256) {
-    const float* gg = i < a.d ? a.gq : a.gk;
-    gam[i] = gg ? gg[i < a.d ? i : i - a.d] : 1.0f;
-  }
-  for (int i = tid; i < 3 * a.R; i += 256) fr[i] = a.freq[i];
-  const int lane = tid & (G - 1), group = tid >> a.lg, groups = 256 >> a.lg;
-  const int first = (tid & ~31) >> a.lg;
-  float acc[2][NIT][2][W];
+  float* gam = sm;                                                  // [2][d]
+  float* red = gam + 2 * a.d;                                       // [8][2][d] gamma sums, at the end
+  float* psum = red + 16 * a.d;                                     // [groups][3] position sums
+  float2* turn = reinterpret_cast<float2*>(psum + 3 * 256);         // [nodes][R]
+  const int tid = threadIdx.x, lane = tid & ((1 << a.lg) - 1), group = tid >> a.lg, nodes = (256 >> a.lg) / a.hs;
+  const int t = group / a.hs, part = group - t * a.hs, H = a.hq + a.hk;
+  LaneUnits<W, NIT> u(a, lane);
+  float acc[2][2][NIT][W];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int j = 0; j < NIT; ++j)
 #pragma unroll
-      for (int i = 0; i < W; ++i) acc[k][j][0][i] = acc[k][j][1][i] = 0.0f;
-
-  for (long long n0 = (long long)blockIdx.x * a.tn; n0 < a.n; n0 += (long long)gridDim.x * a.tn) {
-    const int here = (int)(a.n - n0 < a.tn ? a.n - n0 : a.tn);
+      for (int i = 0; i < W; ++i) acc[k][0][j][i] = acc[k][1][j][i] = 0.0f;
+  const bool want_pos = a.pos_bar && a.R;
+  load_weights(a, gam);
+  for (long long n0 = (long long)blockIdx.x * nodes; n0 < a.n; n0 += (long long)gridDim.x * nodes) {
+    const long long node = n0 + t;
+    const bool there = node < a.n;
+    Pack<T, W> rp[NIT], rq[NIT], sp[NIT], sq[NIT];
+    auto fetch = [&](int h) {
+      const bool live = there && h < H;
+      u.fetch(x + (live ? node * a.ldx + (long long)h * a.d : 0), a.R, live, rp, rq);
+      u.fetch(g + (live ? node * a.ldg + (long long)h * a.d : 0), a.R, live, sp, sq);
+    };
+    fetch(part);
     __syncthreads();
-    for (int i = tid; i < here * a.R; i += 256) {
-      const int t = i / a.R;
-      turn[i] = node_angle(a, n0 + t, i - t * a.R);
-    }
+    load_angles(a, n0, nodes, turn);
     __syncthreads();
+    if (there) u.node(turn + t * a.R);
+    float th[NIT][W];
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      const int Hn = kind == 0 ? a.hq : a.hk, h0 = kind == 0 ? 0 : a.hq;
-      const float* gm = gam + kind * a.d;
-      const int items = here * Hn;
-      for (int base = first; base < items; base += groups) {
-        const int it = base + (group - first);
-        const bool live = it < items;
-        const int t = live ? it / Hn : 0, h = live ? h0 + it - t * Hn : h0;
-        const T* row = x + (n0 + t) * a.ldx + (long long)h * a.d;
-        const T* grow = g + (n0 + t) * a.ldg + (long long)h * a.d;
-        float p[NIT][W], q[NIT][W], gp[NIT][W], gq[NIT][W], ss = 0.0f;
+    for (int j = 0; j < NIT; ++j)
 #pragma unroll
-        for (int j = 0; j < NIT; ++j) {
-          const int u = lane + j * G;
+      for (int i = 0; i < W; ++i) th[j][i] = 0.0f;
+    for (int hb = 0; hb < H; hb += a.hs) {
+      const int h = hb + part;
+      const bool live = there && h < H;
+      const float fk = h < a.hq ? 0.0f : 1.0f, fq = 1.0f - fk;
+      const float* gm = gam + (h < a.hq ? 0 : a.d);
+      const long long hd = (long long)h * a.d;
+      float p[NIT][W], q[NIT][W], gp[NIT][W], gq[NIT][W];
+      u.widen(sp, sq, gp, gq);
+      const float ss = group_sum(u.widen(rp, rq, p, q), a.lg);
+      fetch(h + a.hs);
+      const float r = live ? rsqrtf(ss / (float)a.d + a.eps) : 0.0f;
+      float dot = 0.0f;
 #pragma unroll
-          for (int i = 0; i < W; ++i) p[j][i] = q[j][i] = gp[j][i] = gq[j][i] = 0.0f;
-          if (live && u < a.units) {
-            const int at = unit_at<W>(a, u);
-            load_pack<T, W>(row + at, p[j]);
-            load_pack<T, W>(grow + at, gp[j]);
-            if (at < a.R) {
-              load_pack<T, W>(row + at + a.R, q[j]);
-              load_pack<T, W>(grow + at + a.R, gq[j]);
-            }
+      for (int j = 0; j < NIT; ++j) {
+        if (u.at[j] < 0) continue;
+        float ga[W], gb[W];
+        load_pack<float, W>(gm + u.at[j], ga);
+        if (u.pair[j]) load_pack<float, W>(gm + u.at[j] + a.R, gb);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const float xa = p[j][i] * r;
+          float ua = gp[j][i];
+          p[j][i] = xa;
+          if (u.pair[j]) {
+            const float2 cs = u.cs[j][i];
+            const float xq = q[j][i] * r, ub = gq[j][i] * cs.x - gp[j][i] * cs.y;
+            q[j][i] = xq;
+            ua = gp[j][i] * cs.x + gq[j][i] * cs.y;
+            // g_b y_a - g_a y_b with y turned forward is ub va - ua vb with both turned back
+            th[j][i] += ub * (xa * ga[i]) - ua * (xq * gb[i]);
+            const float c = ub * xq;
+            acc[0][1][j][i] = fmaf(c, fq, acc[0][1][j][i]);
+            acc[1][1][j][i] = fmaf(c, fk, acc[1][1][j][i]);
+            gq[j][i] = ub * gb[i];
+            dot += gq[j][i] * xq;
           }
-#pragma unroll
-          for (int i = 0; i < W; ++i) ss += p[j][i] * p[j][i] + q[j][i] * q[j][i];
+          const float c = ua * xa;
+          acc[0][0][j][i] = fmaf(c, fq, acc[0][0][j][i]);
+          acc[1][0][j][i] = fmaf(c, fk, acc[1][0][j][i]);
+          gp[j][i] = ua * ga[i];
+          dot += gp[j][i] * xa;
         }
-        for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = rsqrtf(ss / (float)a.d + a.eps);
-        float dot = 0.0f, px = 0.0f, py = 0.0f, pz = 0.0f;
+      }
+      const float m = group_sum(dot, a.lg) / (float)a.d;
+      if (!live || !xb) continue;
+      T* out = xb + node * a.ldxb + hd;
 #pragma unroll
-        for (int j = 0; j < NIT; ++j) {
-          const int u = lane + j * G;
-          if (u >= a.units) continue;
-          const int at = unit_at<W>(a, u);
+      for (int j = 0; j < NIT; ++j) {
+        if (u.at[j] < 0) continue;
+        float v[W];
 #pragma unroll
-          for (int i = 0; i < W; ++i) {
-            const float xa = p[j][i] * r, ga = gm[at + i];
-            p[j][i] = xa;
-            float ua = gp[j][i];
-            if (at < a.R) {
-              const float2 cs = turn[t * a.R + at + i];
-              const float xq = q[j][i] * r, gb = gm[at + a.R + i];
-              q[j][i] = xq;
-              const float va = xa * ga, vb = xq * gb;
-              const float ya = va * cs.x - vb * cs.y, yb = va * cs.y + vb * cs.x;
-              const float th = gq[j][i] * ya - gp[j][i] * yb;
-              px += th * fr[at + i];
-              py += th * fr[a.R + at + i];
-              pz += th * fr[2 * a.R + at + i];
-              ua = gp[j][i] * cs.x + gq[j][i] * cs.y;
-              const float ub = gq[j][i] * cs.x - gp[j][i] * cs.y;
-              acc[kind][j][1][i] += ub * xq;
-              gq[j][i] = ub * gb;
-              dot += gq[j][i] * xq;
-            }
-            acc[kind][j][0][i] += ua * xa;
-            gp[j][i] = ua * ga;
-            dot += gp[j][i] * xa;
-          }
-        }
-        for (int o = G >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (a.pos_bar && a.R)
-          for (int o = G >> 1; o > 0; o >>= 1) {
-            px += __shfl_xor_sync(0xffffffffu, px, o);
-            py += __shfl_xor_sync(0xffffffffu, py, o);
-            pz += __shfl_xor_sync(0xffffffffu, pz, o);
-          }
-        if (!live) continue;
-        if (a.pos_bar && a.R && lane == 0) {
-          float* pa = pacc + 3 * (t * H + h);
-          pa[0] = px; pa[1] = py; pa[2] = pz;
-        }
-        if (!xb) continue;
-        const float m = dot / (float)a.d;
-        T* out = xb + (n0 + t) * a.ldxb + (long long)h * a.d;
+        for (int i = 0; i < W; ++i) v[i] = r * (gp[j][i] - p[j][i] * m);
+        store_pack<T, W>(out + u.at[j], v);
+        if (u.pair[j]) {
 #pragma unroll
-        for (int j = 0; j < NIT; ++j) {
-          const int u = lane + j * G;
-          if (u >= a.units) continue;
-          const int at = unit_at<W>(a, u);
-          float v[W];
-#pragma unroll
-          for (int i = 0; i < W; ++i) v[i] = r * (gp[j][i] - p[j][i] * m);
-          store_pack<T, W>(out + at, v);
-          if (at < a.R) {
-#pragma unroll
-            for (int i = 0; i < W; ++i) v[i] = r * (gq[j][i] - q[j][i] * m);
-            store_pack<T, W>(out + at + a.R, v);
-          }
+          for (int i = 0; i < W; ++i) v[i] = r * (gq[j][i] - q[j][i] * m);
+          store_pack<T, W>(out + u.at[j] + a.R, v);
         }
       }
     }
-    if (a.pos_bar && a.R) {
+    if (want_pos) {
+      float v[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < NIT; ++j)
+        if (u.pair[j])
+#pragma unroll
+          for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int c = 0; c < 3; ++c) v[c] += th[j][i] * a.freq[c * a.R + u.at[j] + i];
+#pragma unroll
+      for (int c = 0; c < 3; ++c) v[c] = group_sum(v[c], a.lg);
+      if (lane == 0)
+#pragma unroll
+        for (int c = 0; c < 3; ++c) psum[3 * group + c] = v[c];
       __syncthreads();
-      for (int i = tid; i < here * 3; i += 256) {
-        const int t = i / 3, c = i - 3 * t;
-        float v = 0.0f;
-        for (int h = 0; h < H; ++h) v += pacc[3 * (t * H + h) + c];
-        a.pos_bar[3 * n0 + i] = v;
+      for (int i = tid; i < 3 * nodes; i += 256) {
+        const int n = i / 3, c = i - 3 * n;
+        float s = 0.0f;
+        for (int k = 0; k < a.hs; ++k) s += psum[3 * (n * a.hs + k) + c];
+        if (n0 + n < a.n) a.pos_bar[3 * n0 + i] = s;
       }
     }
   }
   if (!a.gpart) return;
-  // groups of a warp, then warps: [8][2][d] in shared memory
-  __syncthreads();
-  float* red = sm;
+  // groups of a warp, then warps
   for (int i = tid; i < 8 * 2 * a.d; i += 256) red[i] = 0.0f;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int j = 0; j < NIT; ++j) {
-      const int u = lane + j * G;
-      const int at = unit_at<W>(a, u);
+    for (int j = 0; j < NIT; ++j)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        float va = acc[k][j][0][i], vb = acc[k][j][1][i];
-        for (int o = 16; o >= G; o >>= 1) {
+        float va = acc[k][0][j][i], vb = acc[k][1][j][i];
+        for (int o = 16; o >= 1 << a.lg; o >>= 1) {
           va += __shfl_xor_sync(0xffffffffu, va, o);
           vb += __shfl_xor_sync(0xffffffffu, vb, o);
         }
-        if ((tid & 31) < G && u < a.units) {
+        if ((tid & 31) < 1 << a.lg && u.at[j] >= 0) {
           float* to = red + ((tid >> 5) * 2 + k) * a.d;
-          to[at + i] = va;
-          if (at < a.R) to[at + a.R + i] = vb;
+          to[u.at[j] + i] = va;
+          if (u.pair[j]) to[u.at[j] + a.R + i] = vb;
         }
       }
-    }
   __syncthreads();
   for (int i = tid; i < 2 * a.d; i += 256) {
     float v = 0.0f;
@@ -286,24 +328,24 @@ __global__ void __launch_bounds__(256) head_norm_vjp_kernel(HeadArgs a, const T*
 }
 
 // gamma gradients: 32 columns of [blocks][2 d] per block, in a fixed order
-__global__ void __launch_bounds__(256) head_gamma_kernel(int blocks, int d, const float* __restrict__ part,
-                                                         float* __restrict__ gq, float* __restrict__ gk) {
-  __shared__ float sum[8][32];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+__global__ void __launch_bounds__(1024) head_gamma_kernel(int blocks, int d, const float* __restrict__ part,
+                                                          float* __restrict__ gq, float* __restrict__ gk) {
+  __shared__ float sum[32][33];
+  const int l = threadIdx.x & 31, c = blockIdx.x * 32 + l, w = threadIdx.x >> 5;
   float v = 0.0f;
   if (c < 2 * d)
 #pragma unroll 8
-    for (int b = w; b < blocks; b += 8) v += part[(long long)b * 2 * d + c];
-  sum[w][threadIdx.x & 31] = v;
+    for (int b = w; b < blocks; b += 32) v += part[(long long)b * 2 * d + c];
+  sum[w][l] = v;
   __syncthreads();
-  if (w == 0 && c < 2 * d) {
-    float s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s += sum[k][threadIdx.x];
-    if (c < d) {
-      if (gq) gq[c] = s;
+  v = sum[l][w];   // column w of this block
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int col = blockIdx.x * 32 + w;
+  if (l == 0 && col < 2 * d) {
+    if (col < d) {
+      if (gq) gq[col] = v;
     } else if (gk) {
-      gk[c - d] = s;
+      gk[col - d] = v;
     }
   }
 }
@@ -327,38 +369,39 @@ static int unit_width(const fc_head_desc* d) {
   return w;
 }
 
-// Geometry shared by both directions; vjp also keeps one [3] per head and node.
+// Groups: the heads of a node are shared by hs of them, a power of two: a
+// warp's worth, and more while that leaves SMs idle.
 static void head_geom(const fc_head_desc* d, int n, HeadArgs& a) {
   const int W = unit_width(d), H = d->heads_q + d->heads_k;
   a.n = n; a.hq = d->heads_q; a.hk = d->heads_k; a.d = d->head_dim; a.R = d->pairs; a.eps = d->eps;
   a.units = d->pairs / W + (d->head_dim - 2 * d->pairs) / W;
   a.lg = 0;
   while (a.lg < 5 && (1 << a.lg) < a.units) ++a.lg;
-  // four heads per lane group and step, fewer while that leaves SMs idle
-  int tn = (4 * (256 >> a.lg) + H - 1) / H;
-  const int even = n / (2 * device_sm_count());
-  if (tn > even) tn = even;
-  if (tn > 32) tn = 32;
-  a.tn = tn < 1 ? 1 : tn;
+  const int groups = 256 >> a.lg;
+  a.hs = 1;
+  while (2 * a.hs <= H && 2 * a.hs <= groups &&
+         (a.hs < 32 >> a.lg || (long long)n * a.hs / groups < 2 * device_sm_count()))
+    a.hs *= 2;
 }
+static long long head_blocks(const HeadArgs& a) {
+  const int nodes = (256 >> a.lg) / a.hs;
+  return ((long long)a.n + nodes - 1) / nodes;
+}
+static size_t angle_bytes(const HeadArgs& a) { return sizeof(float2) * (size_t)((256 >> a.lg) / a.hs) * a.R; }
 static int vjp_blocks(const HeadArgs& a) {
-  const long long tiles = ((long long)a.n + a.tn - 1) / a.tn;
-  const long long most = 4LL * device_sm_count();
-  return (int)(tiles < most ? tiles : most);
+  const long long all = head_blocks(a), most = 4LL * device_sm_count();
+  return (int)(all < most ? all : most);
 }
 
 template <class T, int W, int NIT>
 static int run_fwd(const HeadArgs& a, const void* x, void* y, cudaStream_t s) {
-  const size_t smem = 8 * (size_t)a.d + 8 * (size_t)a.tn * a.R;
-  const int grid = (int)(((long long)a.n + a.tn - 1) / a.tn);
-  head_norm_kernel<T, W, NIT><<<grid, 256, smem, s>>>(a, static_cast<const T*>(x), static_cast<T*>(y));
+  const size_t smem = sizeof(float) * 2 * a.d + angle_bytes(a);
+  head_norm_kernel<T, W, NIT><<<(unsigned)head_blocks(a), 256, smem, s>>>(a, static_cast<const T*>(x), static_cast<T*>(y));
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
 }
 template <class T, int W, int NIT>
 static int run_vjp(const HeadArgs& a, const void* x, const void* g, void* xb, cudaStream_t s) {
-  size_t smem = 8 * (size_t)a.d + 16 * (size_t)a.R + 8 * (size_t)a.tn * a.R +
-                12 * (size_t)a.tn * (a.hq + a.hk);
-  if (smem < 64 * (size_t)a.d) smem = 64 * (size_t)a.d;
+  const size_t smem = sizeof(float) * (3 * 256 + 18 * (size_t)a.d) + angle_bytes(a);
   head_norm_vjp_kernel<T, W, NIT><<<vjp_blocks(a), 256, smem, s>>>(a, static_cast<const T*>(x),
                                                                    static_cast<const T*>(g), static_cast<T*>(xb));
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
@@ -461,7 +504,7 @@ int fc_head_norm_rotate_vjp(const fc_head_desc* desc, int n_nodes, const void* x
   a.pos_bar = pos_bar;
   const int rc = launch_vjp(desc, a, x, g, x_bar, s);
   if (rc != FC_OK || !gamma) return rc;
-  head_gamma_kernel<<<(2 * D + 31) / 32, 256, 0, s>>>(vjp_blocks(a), D, a.gpart, gamma_q_bar, gamma_k_bar);
+  head_gamma_kernel<<<(2 * D + 31) / 32, 1024, 0, s>>>(vjp_blocks(a), D, a.gpart, gamma_q_bar, gamma_k_bar);
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
 }
 

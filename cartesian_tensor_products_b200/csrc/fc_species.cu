@@ -5,12 +5,13 @@
 // One thread moves 16-byte vectors, a block a run of whole rows.
 //
 // Gradient: table_bar[s] = scale sum of g over the nodes of species s.  The
-// nodes are sorted by species (stable radix sort, one pass of 8 bits for
-// tables below 255 rows), the sorted list is cut into spans of 32 nodes, one
-// warp sums each span and writes the species that lie inside it; a species
-// that crosses spans leaves one partial row per span, which a last kernel adds
-// in span order.  So a species with nearly all nodes costs no more than an
-// even spread, and no sum depends on the order of atomics.
+// nodes are sorted by species (stable radix sort, one pass of 8 bits for tables
+// of up to 255 rows), the sorted list is cut into spans of 32 to 128 nodes, one
+// warp sums each span and writes the species that lie inside it; a species that
+// crosses spans leaves one partial row per span, which a last kernel adds in
+// span order.  That kernel also clears the rows of species without nodes, so
+// that every row is written once.  A species with nearly all nodes costs no
+// more than an even spread, and no sum depends on the order of atomics.
 #include <math.h>
 
 #include "fc_nodes.cuh"
@@ -18,7 +19,6 @@
 namespace fc {
 
 constexpr int kDigits = 256;
-constexpr int kSpan = 32;
 
 // ------------------------------------------------------------------ forward
 
@@ -51,11 +51,15 @@ __global__ void __launch_bounds__(256) species_embed_kernel(int n, int V, int ve
 // --------------------------------------------------------------------- sort
 
 // Chunks of the sort: `rows` nodes each (a multiple of 256), at most 512.
+// Spans of the sums: as long as eight warps per SM allow, since every span of a
+// frequent species leaves a partial row (100,003 nodes of few species, 128
+// channels: joining them took as long as the sums at 32).
 struct SortGeom {
-  int n, V, rows, chunks, passes;
+  int n, V, rows, chunks, passes, span;
 };
-static SortGeom sort_geom(int n, int V) {
-  SortGeom g{n, V, 1024, 0, 1};
+static SortGeom sort_geom(int n, int V, int C) {
+  SortGeom g{n, V, 1024, 0, 1, 32};
+  while (g.span < 128 && (long long)n / (2 * g.span) * ((C + 127) / 128) >= 8 * 148) g.span *= 2;
   const long long per = ((long long)n + 511) / 512;
   if (per > g.rows) g.rows = (int)((per + 255) / 256 * 256);
   g.chunks = (int)(((long long)n + g.rows - 1) / g.rows);
@@ -69,10 +73,9 @@ __device__ __forceinline__ int sort_key(const int32_t* __restrict__ keys, bool r
   return raw && (k < 0 || k >= V) ? V : k;
 }
 
-// Digit counts of every chunk; the first pass also clears table_bar.
+// Digit counts of every chunk.
 __global__ void __launch_bounds__(256) sort_count_kernel(SortGeom g, int shift, bool raw,
-                                                         const int32_t* __restrict__ keys, int* __restrict__ counts,
-                                                         float4* __restrict__ clear, long long clear_n) {
+                                                         const int32_t* __restrict__ keys, int* __restrict__ counts) {
   __shared__ int hist[kDigits];
   hist[threadIdx.x] = 0;
   __syncthreads();
@@ -82,8 +85,6 @@ __global__ void __launch_bounds__(256) sort_count_kernel(SortGeom g, int shift, 
     atomicAdd(&hist[(sort_key(keys, raw, i, g.V) >> shift) & 255], 1);
   __syncthreads();
   counts[blockIdx.x * kDigits + threadIdx.x] = hist[threadIdx.x];
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < clear_n; i += (long long)gridDim.x * 256)
-    clear[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 }
 
 // Stable scatter of one 8-bit digit: a warp owns a contiguous eighth of the
@@ -97,6 +98,7 @@ __global__ void __launch_bounds__(256) sort_scatter_kernel(SortGeom g, int shift
   __shared__ int scan[kDigits];
   const int t = threadIdx.x, w = t >> 5, lane = t & 31;
   int total = 0, before = 0;
+#pragma unroll 8
   for (int c = 0; c < g.chunks; ++c) {
     const int v = counts[c * kDigits + t];
     total += v;
@@ -147,58 +149,65 @@ __global__ void __launch_bounds__(256) sort_scatter_kernel(SortGeom g, int shift
 
 // --------------------------------------------------------------------- sums
 
-// One warp: the sums of one span over one tile of 32 vectors of columns.
+// One warp: the sums of one span over one tile of 128 columns, four per lane (so
+// that the FP32 rows it writes are whole lines for 16-bit gradients too).
 template <class T>
-__global__ void __launch_bounds__(256) span_sum_kernel(int n, int V, int C, long long ldg, float scale,
+__global__ void __launch_bounds__(256) span_sum_kernel(int n, int V, int C, int span_rows, long long ldg, float scale,
                                                        const int32_t* __restrict__ keys,
                                                        const int32_t* __restrict__ idx, const T* __restrict__ g,
                                                        float* __restrict__ bar, float* __restrict__ part) {
-  constexpr int W = RowType<T>::kVec;
   const int lane = threadIdx.x & 31;
   const long long span = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const long long start = span * kSpan;
+  const long long start = span * span_rows;
   if (start >= n) return;
-  const int cnt = (int)(n - start < kSpan ? n - start : kSpan);
-  const int col = (blockIdx.y * 32 + lane) * W;
+  const int cnt = (int)(n - start < span_rows ? n - start : span_rows);
+  const int col = blockIdx.y * 128 + lane * 4;
   const bool in = col < C;
-  const int key = lane < cnt ? keys[start + lane] : -1;
-  const int row = lane < cnt ? idx[start + lane] : 0;
   const int prev = start > 0 ? keys[start - 1] : -1;
   const int next = start + cnt < n ? keys[start + cnt] : -1;
-  float acc[W];
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   int cur = -1;
   bool begins = false;
   auto flush = [&](bool ends) {
     if (cur < 0 || cur >= V || !in) return;
     float* to = begins && ends ? bar + (long long)cur * C : part + (2 * span + (begins ? 1 : 0)) * C;
     const float f = begins && ends ? scale : 1.0f;
-#pragma unroll
-    for (int k = 0; k < W; k += 4)
-      *reinterpret_cast<float4*>(to + col + k) = make_float4(acc[k] * f, acc[k + 1] * f, acc[k + 2] * f, acc[k + 3] * f);
+    *reinterpret_cast<float4*>(to + col) = make_float4(acc[0] * f, acc[1] * f, acc[2] * f, acc[3] * f);
   };
-  constexpr int U = 8;   // rows in flight per lane
-  for (int r0 = 0; r0 < cnt; r0 += U) {
-    float v[U][W];
+  // Every load is made (rows past the span repeat its first, lanes past the
+  // columns read column 0), so that they go out together.
+  constexpr int U = 16;   // rows in flight per lane
+  const T* gc = g + (in ? col : 0);
+  int key = 0, row = 0;
+  auto next_rows = [&](int b0) {
+    const long long at = start + (b0 + lane < cnt ? b0 + lane : 0);
+    key = keys[at];
+    row = idx[at];
+  };
+  next_rows(0);
+  for (int b0 = 0; b0 < cnt; b0 += 32) {
+    const int k32 = key, r32 = row;
+    next_rows(b0 + 32);
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32 && b0 + r0 < cnt; r0 += U) {
+      float v[U][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int rr = __shfl_sync(0xffffffffu, row, r0 + u);
+      for (int u = 0; u < U; ++u)
+        load_pack<T, 4>(gc + (long long)__shfl_sync(0xffffffffu, r32, r0 + u) * ldg, v[u]);
 #pragma unroll
-      for (int k = 0; k < W; ++k) v[u][k] = 0.0f;
-      if (in && r0 + u < cnt) load_pack<T, W>(g + rr * ldg + col, v[u]);
-    }
+      for (int u = 0; u < U; ++u) {
+        const int k = __shfl_sync(0xffffffffu, k32, r0 + u);
+        if (b0 + r0 + u < cnt) {
+          if (k != cur || cur < 0) {
+            flush(true);
+            cur = k;
+            begins = b0 + r0 + u > 0 || prev != k;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = __shfl_sync(0xffffffffu, key, r0 + u);
-      if (r0 + u < cnt) {
-        if (k != cur || r0 + u == 0) {
-          flush(true);
-          cur = k;
-          begins = r0 + u > 0 || prev != k;
+            for (int i = 0; i < 4; ++i) acc[i] = 0.0f;
+          }
 #pragma unroll
-          for (int i = 0; i < W; ++i) acc[i] = 0.0f;
+          for (int i = 0; i < 4; ++i) acc[i] += v[u][i];
         }
-#pragma unroll
-        for (int i = 0; i < W; ++i) acc[i] += v[u][i];
       }
     }
   }
@@ -207,18 +216,40 @@ __global__ void __launch_bounds__(256) span_sum_kernel(int n, int V, int C, long
 
 // Joins the species that cross spans.  A warp looks at one span: if a species
 // begins in it and runs on, the warp adds its partial rows (at most 64 spans;
-// longer ones are added by the whole block).
-__global__ void __launch_bounds__(1024) span_join_kernel(int n, int V, int C, float scale,
+// longer ones are added by the whole block).  Blocks from join_blocks on clear
+// the species without nodes: a lane searches one species in the sorted list.
+__global__ void __launch_bounds__(1024) span_join_kernel(int n, int V, int C, int span_rows, int join_blocks, float scale,
                                                          const int32_t* __restrict__ keys,
                                                          const float* __restrict__ part, float* __restrict__ bar) {
   __shared__ int lng[32];
   __shared__ float sum[32][128];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long spans = ((long long)n + kSpan - 1) / kSpan;
+  const long long spans = ((long long)n + span_rows - 1) / span_rows;
   const long long s = (long long)blockIdx.x * 32 + w;
   const int col = blockIdx.y * 128 + lane * 4;
   const bool in = col < C;
-  auto head = [&](long long sp) { return keys[sp * kSpan]; };
+  if ((int)blockIdx.x >= join_blocks) {
+    const long long v = ((long long)(blockIdx.x - join_blocks) * 32 + w) * 32 + lane;
+    bool none = false;
+    if (v < V) {
+      int lo = 0, hi = n;   // first node of species >= v
+      while (lo < hi) {
+        const int mid = (int)(((unsigned)lo + (unsigned)hi) >> 1);
+        if (keys[mid] < v)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      none = lo == n || keys[lo] != v;
+    }
+    unsigned todo = __ballot_sync(0xffffffffu, none);
+    for (; todo; todo &= todo - 1) {
+      const long long row = v - lane + (__ffs(todo) - 1);
+      if (in) *reinterpret_cast<float4*>(bar + row * C + col) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    return;
+  }
+  auto head = [&](long long sp) { return keys[sp * span_rows]; };
   auto add = [&](float4& a, long long slot) {
     const float4 v = *reinterpret_cast<const float4*>(part + slot * C + col);
     a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
@@ -226,9 +257,9 @@ __global__ void __launch_bounds__(1024) span_join_kernel(int n, int V, int C, fl
   if (lane == 0) lng[w] = 0;
   int k = -1;
   if (s + 1 < spans) {
-    k = keys[(s + 1) * kSpan - 1];
+    k = keys[(s + 1) * span_rows - 1];
     const bool runs_on = head(s + 1) == k;
-    const bool begins = head(s) != k || s == 0 || keys[s * kSpan - 1] != k;
+    const bool begins = head(s) != k || s == 0 || keys[s * span_rows - 1] != k;
     if (!runs_on || !begins || k >= V) k = -1;
   }
   if (k >= 0) {
@@ -256,7 +287,7 @@ __global__ void __launch_bounds__(1024) span_join_kernel(int n, int V, int C, fl
   for (int j = 0; j < 32; ++j) {
     if (!lng[j]) continue;
     const long long sj = (long long)blockIdx.x * 32 + j;
-    const int kj = keys[(sj + 1) * kSpan - 1];
+    const int kj = keys[(sj + 1) * span_rows - 1];
     long long m = 0;
     int run = 1024;
     while (run == 1024) {
@@ -290,7 +321,7 @@ struct EmbedLayout {
 };
 static EmbedLayout embed_layout(int n, int V, int C) {
   EmbedLayout l;
-  l.g = sort_geom(n, V);
+  l.g = sort_geom(n, V, C);
   size_t at = 0;
   const size_t list = round16(4 * (size_t)n);
   for (int i = 0; i < 2; ++i) {
@@ -302,7 +333,7 @@ static EmbedLayout embed_layout(int n, int V, int C) {
   l.counts = at;
   at += 4 * (size_t)kDigits * l.g.chunks;
   l.part = at;
-  at += 2 * (((size_t)n + kSpan - 1) / kSpan) * C * 4;
+  at += 2 * (((size_t)n + l.g.span - 1) / l.g.span) * C * 4;
   l.bytes = at;
   return l;
 }
@@ -334,10 +365,9 @@ static int embed_fwd(int n, int V, int lmax, int C, float scale, const int32_t* 
 template <class T>
 static void span_sum(const EmbedLayout& l, int C, long long ldg, float scale, const int32_t* keys, const int32_t* idx,
                      const void* g, float* bar, float* part, cudaStream_t s) {
-  const long long spans = ((long long)l.g.n + kSpan - 1) / kSpan;
-  const int tile = 32 * RowType<T>::kVec;
-  span_sum_kernel<T><<<dim3((unsigned)((spans + 7) / 8), (C + tile - 1) / tile), 256, 0, s>>>(
-      l.g.n, l.g.V, C, ldg, scale, keys, idx, static_cast<const T*>(g), bar, part);
+  const long long spans = ((long long)l.g.n + l.g.span - 1) / l.g.span;
+  span_sum_kernel<T><<<dim3((unsigned)((spans + 7) / 8), (C + 127) / 128), 256, 0, s>>>(
+      l.g.n, l.g.V, C, l.g.span, ldg, scale, keys, idx, static_cast<const T*>(g), bar, part);
 }
 
 }  // namespace fc
@@ -387,8 +417,7 @@ int fc_species_embed_vjp(int dtype, int n_nodes, int n_species, int lmax, int ch
   for (int p = 0; p < l.g.passes; ++p) {
     int32_t* okeys = reinterpret_cast<int32_t*>(ws + l.keys[p & 1]);
     int32_t* oidx = reinterpret_cast<int32_t*>(ws + l.idx[p & 1]);
-    sort_count_kernel<<<l.g.chunks, 256, 0, s>>>(l.g, 8 * p, p == 0, keys, counts, reinterpret_cast<float4*>(table_bar),
-                                                 p == 0 ? (long long)(bar_bytes / 16) : 0);
+    sort_count_kernel<<<l.g.chunks, 256, 0, s>>>(l.g, 8 * p, p == 0, keys, counts);
     sort_scatter_kernel<<<l.g.chunks, 256, 0, s>>>(l.g, 8 * p, p == 0, keys, idx, counts, okeys, oidx);
     keys = okeys;
     idx = oidx;
@@ -400,10 +429,10 @@ int fc_species_embed_vjp(int dtype, int n_nodes, int n_species, int lmax, int ch
     span_sum<__nv_bfloat16>(l, channels, ldg, scale, keys, idx, g, table_bar, part, s);
   else
     span_sum<__half>(l, channels, ldg, scale, keys, idx, g, table_bar, part, s);
-  const long long spans = ((long long)n_nodes + kSpan - 1) / kSpan;
-  if (spans > 1)
-    span_join_kernel<<<dim3((unsigned)((spans + 31) / 32), (channels + 127) / 128), 1024, 0, s>>>(
-        n_nodes, n_species, channels, scale, keys, part, table_bar);
+  const long long spans = ((long long)n_nodes + l.g.span - 1) / l.g.span;
+  const int join = spans > 1 ? (int)((spans + 31) / 32) : 0, clear = (int)(((long long)n_species + 1023) / 1024);
+  span_join_kernel<<<dim3((unsigned)(join + clear), (channels + 127) / 128), 1024, 0, s>>>(
+      n_nodes, n_species, channels, l.g.span, join, scale, keys, part, table_bar);
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
 }
 
