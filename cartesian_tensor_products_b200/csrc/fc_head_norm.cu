@@ -13,25 +13,37 @@
 // turns, since FP32 would lose the phase of positions far from the origin.
 #include <math.h>
 
+#include "fc_device.cuh"
 #include "fc_nodes.cuh"
 
 namespace fc {
 
 struct HeadArgs {
   int n, hq, hk, d, R, units, lg, hs;   // lg: log2 of the lanes of a group; hs: groups that share a node's heads
-  float eps;
+  float eps, inv_d;
   long long ldx, ldy, ldg, ldxb;
   const float *gq, *gk, *pos, *freq;
   float *gpart, *pos_bar;
 };
 
-// cos and sin of angle f of a node
-__device__ __forceinline__ float2 node_angle(const HeadArgs& a, const double (&p)[3], int f) {
-  const double th = p[0] * a.freq[f] + p[1] * a.freq[a.R + f] + p[2] * a.freq[2 * a.R + f];
-  const double t = th * 0.31830988618379067154;   // half turns
-  float s, c;
-  sincospif((float)(t - 2.0 * rint(0.5 * t)), &s, &c);
-  return make_float2(c, s);
+// cos and sin of t half turns.  The quarter turns are taken off in FP64 (adding
+// and subtracting 1.5 2^52 rounds to a whole number, whose low bits are the
+// quadrant), the rest |f| <= 1/4 goes through polynomials in f^2 of least
+// largest error (fitted to sin(pi f)/f, relative, 3.2e-9, and cos(pi f), 4.7e-11).
+__device__ __forceinline__ float2 half_turns(double t) {
+  constexpr double kRound = 6755399441055744.0;
+  const double m = fma(t, 2.0, kRound);
+  const int quad = __double2loint(m);
+  const float f = (float)fma(m - kRound, -0.5, t), z = f * f;
+  float s = fmaf(z, -0.5890122f, 2.549761f);
+  s = fmaf(z, s, -5.167708f);
+  s = f * fmaf(z, s, 3.1415927f);
+  float c = fmaf(z, 0.23132971f, -1.3350446f);
+  c = fmaf(z, c, 4.058707f);
+  c = fmaf(z, c, -4.934802f);
+  c = fmaf(z, c, 1.0f);
+  const float x = quad & 1 ? s : c, y = quad & 1 ? c : s;   // quarter turn: cos -> -sin, sin -> cos
+  return make_float2((quad + 1) & 2 ? -x : x, quad & 2 ? -y : y);
 }
 
 // First value of unit u: rotated pairs first (partner at + R), then the rest.
@@ -41,12 +53,88 @@ __device__ __forceinline__ int unit_at(const HeadArgs& a, int u) {
   return u < p ? u * W : 2 * a.R + (u - p) * W;
 }
 
+// Arithmetic on the W values of a unit, two per instruction (both kernels are
+// bound by instructions before they are by memory at one value each).
+template <int W>
+__device__ __forceinline__ void vmul(const float (&a)[W], const float (&b)[W], float (&o)[W]) {
+  if constexpr (W % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {
+      const float2 v = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+      o[i] = v.x;
+      o[i + 1] = v.y;
+    }
+  } else {
+    o[0] = a[0] * b[0];
+  }
+}
+template <int W>
+__device__ __forceinline__ void vscale(const float (&a)[W], float f, float (&o)[W]) {
+  if constexpr (W % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {
+      const float2 v = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(f, f));
+      o[i] = v.x;
+      o[i + 1] = v.y;
+    }
+  } else {
+    o[0] = a[0] * f;
+  }
+}
+// o = a b + c
+template <int W>
+__device__ __forceinline__ void vfma(const float (&a)[W], const float (&b)[W], const float (&c)[W], float (&o)[W]) {
+  if constexpr (W % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {
+      const float2 v = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), make_float2(c[i], c[i + 1]));
+      o[i] = v.x;
+      o[i + 1] = v.y;
+    }
+  } else {
+    o[0] = fmaf(a[0], b[0], c[0]);
+  }
+}
+// o = a f + c
+template <int W>
+__device__ __forceinline__ void vfmas(const float (&a)[W], float f, const float (&c)[W], float (&o)[W]) {
+  if constexpr (W % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {
+      const float2 v = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(f, f), make_float2(c[i], c[i + 1]));
+      o[i] = v.x;
+      o[i + 1] = v.y;
+    }
+  } else {
+    o[0] = fmaf(a[0], f, c[0]);
+  }
+}
+// o = a b - c d
+template <int W>
+__device__ __forceinline__ void vcross(const float (&a)[W], const float (&b)[W], const float (&c)[W],
+                                       const float (&d)[W], float (&o)[W]) {
+  float t[W];
+  vmul(c, d, t);
+#pragma unroll
+  for (int i = 0; i < W; ++i) o[i] = fmaf(a[i], b[i], -t[i]);
+}
+// s += sum of a b, in two chains
+template <int W>
+__device__ __forceinline__ void vdot(const float (&a)[W], const float (&b)[W], float2& s) {
+  if constexpr (W % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < W; i += 2) s = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), s);
+  } else {
+    s.x = fmaf(a[0], b[0], s.x);
+  }
+}
+
 // What a lane keeps of a node: its units' places and angles.
 template <int W, int NIT>
 struct LaneUnits {
   int at[NIT];          // -1: no unit
   bool pair[NIT];
-  float2 cs[NIT][W];
+  float c[NIT][W], s[NIT][W];
 
   __device__ __forceinline__ LaneUnits(const HeadArgs& a, int lane) {
 #pragma unroll
@@ -55,7 +143,10 @@ struct LaneUnits {
       at[j] = u < a.units ? unit_at<W>(a, u) : -1;
       pair[j] = at[j] >= 0 && at[j] < a.R;
 #pragma unroll
-      for (int i = 0; i < W; ++i) cs[j][i] = make_float2(1.0f, 0.0f);
+      for (int i = 0; i < W; ++i) {
+        c[j][i] = 1.0f;
+        s[j][i] = 0.0f;
+      }
     }
   }
   // angles of a node from the block's table
@@ -64,108 +155,158 @@ struct LaneUnits {
     for (int j = 0; j < NIT; ++j)
       if (pair[j])
 #pragma unroll
-        for (int i = 0; i < W; ++i) cs[j][i] = turn[at[j] + i];
+        for (int i = 0; i < W; ++i) {
+          const float2 t = turn[at[j] + i];
+          c[j][i] = t.x;
+          s[j][i] = t.y;
+        }
   }
-  // a head's values as they are stored, zeros where the lane has none
+  // a head's values as they are stored; what the lane has no unit for stays as
+  // it is (clear), a head that is not there is zeros
   template <class T>
-  __device__ __forceinline__ void fetch(const T* row, int R, bool live, Pack<T, W> (&p)[NIT], Pack<T, W> (&q)[NIT]) const {
+  static __device__ __forceinline__ void clear(Pack<T, W> (&p)[NIT], Pack<T, W> (&q)[NIT]) {
 #pragma unroll
     for (int j = 0; j < NIT; ++j) {
       p[j].clear();
       q[j].clear();
-      if (live && at[j] >= 0) p[j] = *reinterpret_cast<const Pack<T, W>*>(row + at[j]);
-      if (live && pair[j]) q[j] = *reinterpret_cast<const Pack<T, W>*>(row + at[j] + R);
+    }
+  }
+  template <class T>
+  __device__ __forceinline__ void fetch(const T* row, int R, bool live, Pack<T, W> (&p)[NIT], Pack<T, W> (&q)[NIT]) const {
+#pragma unroll
+    for (int j = 0; j < NIT; ++j) {
+      if (live) {
+        if (at[j] >= 0) p[j] = *reinterpret_cast<const Pack<T, W>*>(row + at[j]);
+        if (pair[j]) q[j] = *reinterpret_cast<const Pack<T, W>*>(row + at[j] + R);
+      } else {
+        p[j].clear();
+        q[j].clear();
+      }
     }
   }
   // to FP32; the sum of squares
   template <class T>
   __device__ __forceinline__ float widen(const Pack<T, W> (&a)[NIT], const Pack<T, W> (&b)[NIT], float (&p)[NIT][W],
                                          float (&q)[NIT][W]) const {
-    float ss = 0.0f;
+    float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < NIT; ++j) {
       a[j].get(p[j]);
       b[j].get(q[j]);
-#pragma unroll
-      for (int i = 0; i < W; ++i) ss += p[j][i] * p[j][i] + q[j][i] * q[j][i];
+      vdot(p[j], p[j], ss);
+      vdot(q[j], q[j], ss);
     }
-    return ss;
+    return ss.x + ss.y;
   }
 };
 
 __device__ __forceinline__ float group_sum(float v, int lg) {
-  for (int o = (1 << lg) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lg > 0) v += __shfl_xor_sync(0xffffffffu, v, 1);
+  if (lg > 1) v += __shfl_xor_sync(0xffffffffu, v, 2);
+  if (lg > 2) v += __shfl_xor_sync(0xffffffffu, v, 4);
+  if (lg > 3) v += __shfl_xor_sync(0xffffffffu, v, 8);
+  if (lg > 4) v += __shfl_xor_sync(0xffffffffu, v, 16);
   return v;
 }
-// the weights of both kinds, [2][d], and the angles of a block's nodes from n0 on, [nodes][R]
-__device__ __forceinline__ void load_weights(const HeadArgs& a, float* gam) {
+// One thread's part of the angle table: frequency f of the nodes first, first +
+// stride, ..
+struct Angles {
+  int f, first, stride;
+  double w[3];   // frequency in half turns per unit of length
+  __device__ __forceinline__ explicit Angles(const HeadArgs& a) {
+    f = first = 0;
+    stride = 1 << 30;
+    if (a.R == 0) {
+      first = stride;
+      return;
+    }
+    const int rows = 256 / a.R;   // R <= 64
+    first = threadIdx.x / a.R;
+    f = threadIdx.x - first * a.R;
+    stride = first < rows ? rows : stride;
+    if (first >= rows) first = stride;
+#pragma unroll
+    for (int c = 0; c < 3; ++c) w[c] = (double)a.freq[c * a.R + f] * 0.31830988618379067154;
+  }
+  // the angles of nodes n0 .. n0 + nodes - 1, [nodes][R]
+  __device__ __forceinline__ void table(const HeadArgs& a, long long n0, int nodes, float2* turn) const {
+    for (int t = first; t < nodes && n0 + t < a.n; t += stride) {
+      const float* p = a.pos + 3 * (n0 + t);
+      turn[t * a.R + f] = half_turns(fma((double)p[0], w[0], fma((double)p[1], w[1], (double)p[2] * w[2])));
+    }
+  }
+};
+// gamma of both kinds in shared memory, [2][d] (16-byte aligned there, which
+// the caller's need not be)
+__device__ __forceinline__ void block_weights(const HeadArgs& a, float* gam) {
   for (int i = threadIdx.x; i < 2 * a.d; i += 256) {
     const float* g = i < a.d ? a.gq : a.gk;
     gam[i] = g ? g[i < a.d ? i : i - a.d] : 1.0f;
   }
 }
-__device__ __forceinline__ void load_angles(const HeadArgs& a, long long n0, int nodes, float2* turn) {
-  for (int i = threadIdx.x; i < nodes * a.R; i += 256) {
-    const int t = i / a.R;
-    const long long n = n0 + t;
-    if (n >= a.n) break;
-    const double p[3] = {a.pos[3 * n], a.pos[3 * n + 1], a.pos[3 * n + 2]};
-    turn[i] = node_angle(a, p, i - t * a.R);
-  }
-}
-
 template <class T, int W, int NIT>
-__global__ void __launch_bounds__(256) head_norm_kernel(HeadArgs a, const T* __restrict__ x, T* __restrict__ y) {
+__global__ void __launch_bounds__(256, 3) head_norm_kernel(HeadArgs a, const T* __restrict__ x, T* __restrict__ y) {
   extern __shared__ float sm[];
-  float* gam = sm;
-  float2* turn = reinterpret_cast<float2*>(sm + 2 * a.d);
+  float* gam = sm;                                          // [2][d]
+  float2* turn = reinterpret_cast<float2*>(sm + 2 * a.d);   // [nodes][R]
   const int lane = threadIdx.x & ((1 << a.lg) - 1), group = threadIdx.x >> a.lg, nodes = (256 >> a.lg) / a.hs;
   const long long n0 = (long long)blockIdx.x * nodes;
-  const int t = group / a.hs, part = group - t * a.hs, H = a.hq + a.hk;
+  const int t = group / a.hs, part = group - t * a.hs;
   const long long node = n0 + t;
   const bool there = node < a.n;
   LaneUnits<W, NIT> u(a, lane);
-  // a head's loads run beside the work on the one before (the first's beside the angles)
+  // The group's heads: part, part + hs, .. of the queries, then of the keys.  A
+  // head's loads run beside the work on the one before (the first's beside the
+  // angles).
+  const T* xr = x + (there ? node * a.ldx + (long long)part * a.d : 0);
+  T* yr = y + (there ? node * a.ldy + (long long)part * a.d : 0);
   Pack<T, W> rp[NIT], rq[NIT];
-  auto fetch = [&](int h) {
-    const bool live = there && h < H;
-    u.fetch(x + (live ? node * a.ldx + (long long)h * a.d : 0), a.R, live, rp, rq);
-  };
-  fetch(part);
-  load_weights(a, gam);
-  load_angles(a, n0, nodes, turn);
+  u.clear(rp, rq);
+  auto fetch = [&](int h, int Hn) { u.fetch(xr, a.R, there && h < Hn, rp, rq); };
+  fetch(part, a.hq ? a.hq : a.hk);
+  block_weights(a, gam);
+  const Angles angles(a);
+  angles.table(a, n0, nodes, turn);
   __syncthreads();
   if (there) u.node(turn + t * a.R);
-  for (int hb = 0; hb < H; hb += a.hs) {   // the same count in every lane
-    const int h = hb + part;
-    const bool live = there && h < H;
-    const long long hd = (long long)h * a.d;
-    float p[NIT][W], q[NIT][W];
-    const float ss = group_sum(u.widen(rp, rq, p, q), a.lg);
-    fetch(h + a.hs);
-    const float r = rsqrtf(ss / (float)a.d + a.eps);
-    if (!live) continue;
-    const float* gm = gam + (h < a.hq ? 0 : a.d);
-    T* out = y + node * a.ldy + hd;
+  const int step = a.hs * a.d;
 #pragma unroll
-    for (int j = 0; j < NIT; ++j) {
-      if (u.at[j] < 0) continue;
-      float v[W], w[W], ga[W], gb[W];
-      load_pack<float, W>(gm + u.at[j], ga);
-      if (u.pair[j]) {
-        load_pack<float, W>(gm + u.at[j] + a.R, gb);
+  for (int kind = 0; kind < 2; ++kind) {
+    const int Hn = kind == 0 ? a.hq : a.hk;
+    if (Hn == 0) continue;
+    const float* gm = gam + kind * a.d;
+    for (int hb = 0; hb < Hn; hb += a.hs) {   // the same count in every lane
+      const bool live = there && hb + part < Hn, last = hb + a.hs >= Hn;
+      float p[NIT][W], q[NIT][W];
+      const float ss = group_sum(u.widen(rp, rq, p, q), a.lg);
+      const int move = last && kind == 0 ? a.hq * a.d - hb * a.d : step;   // to the group's next head
+      xr += move;
+      if (!last)
+        fetch(hb + a.hs + part, Hn);
+      else if (kind == 0)
+        fetch(part, a.hk);
+      const float r = rsqrtf(ss * a.inv_d + a.eps);
+      if (live) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const float ua = p[j][i] * r * ga[i], ub = q[j][i] * r * gb[i];
-          v[i] = ua * u.cs[j][i].x - ub * u.cs[j][i].y;
-          w[i] = ua * u.cs[j][i].y + ub * u.cs[j][i].x;
+        for (int j = 0; j < NIT; ++j) {
+          if (u.at[j] < 0) continue;
+          float v[W], w[W], gw[W];
+          load_pack<float, W>(gm + u.at[j], gw);
+          vscale(p[j], r, p[j]);
+          vmul(p[j], gw, v);
+          if (u.pair[j]) {
+            vscale(q[j], r, q[j]);
+            load_pack<float, W>(gm + u.at[j] + a.R, gw);
+            vmul(q[j], gw, q[j]);   // v and q: the normed pair
+            vmul(v, u.s[j], w);
+            vfma(q[j], u.c[j], w, w);
+            vcross(v, u.c[j], q[j], u.s[j], v);
+            store_pack<T, W>(yr + u.at[j] + a.R, w);
+          }
+          store_pack<T, W>(yr + u.at[j], v);
         }
-        store_pack<T, W>(out + u.at[j] + a.R, w);
-      } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = p[j][i] * r * ga[i];
       }
-      store_pack<T, W>(out + u.at[j], v);
+      yr += move;
     }
   }
 }
@@ -180,12 +321,16 @@ __global__ void __launch_bounds__(256, 2) head_norm_vjp_kernel(HeadArgs a, const
                                                                const T* __restrict__ g, T* __restrict__ xb) {
   extern __shared__ float sm[];
   float* gam = sm;                                                  // [2][d]
-  float* red = gam + 2 * a.d;                                       // [8][2][d] gamma sums, at the end
+  float* red = gam + 2 * a.d;                                       // [8][2][d] gamma sums
   float* psum = red + 16 * a.d;                                     // [groups][3] position sums
   float2* turn = reinterpret_cast<float2*>(psum + 3 * 256);         // [nodes][R]
   const int tid = threadIdx.x, lane = tid & ((1 << a.lg) - 1), group = tid >> a.lg, nodes = (256 >> a.lg) / a.hs;
-  const int t = group / a.hs, part = group - t * a.hs, H = a.hq + a.hk;
+  const int t = group / a.hs, part = group - t * a.hs;
   LaneUnits<W, NIT> u(a, lane);
+  const Angles angles(a);
+  const bool want_pos = a.pos_bar && a.R;
+  const int step = a.hs * a.d;
+  block_weights(a, gam);
   float acc[2][2][NIT][W];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
@@ -193,20 +338,23 @@ __global__ void __launch_bounds__(256, 2) head_norm_vjp_kernel(HeadArgs a, const
     for (int j = 0; j < NIT; ++j)
 #pragma unroll
       for (int i = 0; i < W; ++i) acc[k][0][j][i] = acc[k][1][j][i] = 0.0f;
-  const bool want_pos = a.pos_bar && a.R;
-  load_weights(a, gam);
   for (long long n0 = (long long)blockIdx.x * nodes; n0 < a.n; n0 += (long long)gridDim.x * nodes) {
     const long long node = n0 + t;
     const bool there = node < a.n;
+    const long long h0 = (long long)part * a.d;
+    const T* xr = x + (there ? node * a.ldx + h0 : 0);
+    const T* gr = g + (there ? node * a.ldg + h0 : 0);
+    T* br = xb + (there ? node * a.ldxb + h0 : 0);
     Pack<T, W> rp[NIT], rq[NIT], sp[NIT], sq[NIT];
-    auto fetch = [&](int h) {
-      const bool live = there && h < H;
-      u.fetch(x + (live ? node * a.ldx + (long long)h * a.d : 0), a.R, live, rp, rq);
-      u.fetch(g + (live ? node * a.ldg + (long long)h * a.d : 0), a.R, live, sp, sq);
+    u.clear(rp, rq);
+    u.clear(sp, sq);
+    auto fetch = [&](int h, int Hn) {
+      u.fetch(xr, a.R, there && h < Hn, rp, rq);
+      u.fetch(gr, a.R, there && h < Hn, sp, sq);
     };
-    fetch(part);
+    fetch(part, a.hq ? a.hq : a.hk);
     __syncthreads();
-    load_angles(a, n0, nodes, turn);
+    angles.table(a, n0, nodes, turn);
     __syncthreads();
     if (there) u.node(turn + t * a.R);
     float th[NIT][W];
@@ -214,64 +362,74 @@ __global__ void __launch_bounds__(256, 2) head_norm_vjp_kernel(HeadArgs a, const
     for (int j = 0; j < NIT; ++j)
 #pragma unroll
       for (int i = 0; i < W; ++i) th[j][i] = 0.0f;
-    for (int hb = 0; hb < H; hb += a.hs) {
-      const int h = hb + part;
-      const bool live = there && h < H;
-      const float fk = h < a.hq ? 0.0f : 1.0f, fq = 1.0f - fk;
-      const float* gm = gam + (h < a.hq ? 0 : a.d);
-      const long long hd = (long long)h * a.d;
-      float p[NIT][W], q[NIT][W], gp[NIT][W], gq[NIT][W];
-      u.widen(sp, sq, gp, gq);
-      const float ss = group_sum(u.widen(rp, rq, p, q), a.lg);
-      fetch(h + a.hs);
-      const float r = live ? rsqrtf(ss / (float)a.d + a.eps) : 0.0f;
-      float dot = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NIT; ++j) {
-        if (u.at[j] < 0) continue;
-        float ga[W], gb[W];
-        load_pack<float, W>(gm + u.at[j], ga);
-        if (u.pair[j]) load_pack<float, W>(gm + u.at[j] + a.R, gb);
+    for (int kind = 0; kind < 2; ++kind) {
+      const int Hn = kind == 0 ? a.hq : a.hk;
+      if (Hn == 0) continue;
+      const float* gm = gam + kind * a.d;
+      for (int hb = 0; hb < Hn; hb += a.hs) {   // the same count in every lane
+        const bool live = there && hb + part < Hn;
+        float p[NIT][W], q[NIT][W], gp[NIT][W], gq[NIT][W];
+        u.widen(sp, sq, gp, gq);
+        const float ss = group_sum(u.widen(rp, rq, p, q), a.lg);
+        const bool last = hb + a.hs >= Hn;
+        const int move = last && kind == 0 ? a.hq * a.d - hb * a.d : step;   // to the group's next head
+        xr += move;
+        gr += move;
+        if (!last)
+          fetch(hb + a.hs + part, Hn);
+        else if (kind == 0)
+          fetch(part, a.hk);
+        const float r = live ? rsqrtf(ss * a.inv_d + a.eps) : 0.0f;
+        float2 dots = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const float xa = p[j][i] * r;
-          float ua = gp[j][i];
-          p[j][i] = xa;
+        for (int j = 0; j < NIT; ++j) {
+          if (u.at[j] < 0) continue;
+          float ga[W];
+          load_pack<float, W>(gm + u.at[j], ga);
+          vscale(p[j], r, p[j]);
           if (u.pair[j]) {
-            const float2 cs = u.cs[j][i];
-            const float xq = q[j][i] * r, ub = gq[j][i] * cs.x - gp[j][i] * cs.y;
-            q[j][i] = xq;
-            ua = gp[j][i] * cs.x + gq[j][i] * cs.y;
-            // g_b y_a - g_a y_b with y turned forward is ub va - ua vb with both turned back
-            th[j][i] += ub * (xa * ga[i]) - ua * (xq * gb[i]);
-            const float c = ub * xq;
-            acc[0][1][j][i] = fmaf(c, fq, acc[0][1][j][i]);
-            acc[1][1][j][i] = fmaf(c, fk, acc[1][1][j][i]);
-            gq[j][i] = ub * gb[i];
-            dot += gq[j][i] * xq;
+            float t1[W], t2[W], gb[W];
+            vscale(q[j], r, q[j]);
+            // turned back: (ua, ub) = (g_a c + g_b s, g_b c - g_a s)
+            vmul(gq[j], u.s[j], t1);
+            vfma(gp[j], u.c[j], t1, t2);
+            vcross(gq[j], u.c[j], gp[j], u.s[j], gq[j]);
+#pragma unroll
+            for (int i = 0; i < W; ++i) gp[j][i] = t2[i];
+            vfma(gq[j], q[j], acc[kind][1][j], acc[kind][1][j]);
+            // g_b y_a - g_a y_b with y turned forward is ub va - ua vb with both
+            // turned back; va = xa ga, vb = xb gb, and ga, gb go into ub, ua
+            load_pack<float, W>(gm + u.at[j] + a.R, gb);
+            vmul(gq[j], ga, t1);
+            vfma(t1, p[j], th[j], th[j]);
+            vmul(gp[j], gb, t1);
+#pragma unroll
+            for (int i = 0; i < W; ++i) th[j][i] = fmaf(-t1[i], q[j][i], th[j][i]);
+            vmul(gq[j], gb, gq[j]);
+            vdot(gq[j], q[j], dots);
           }
-          const float c = ua * xa;
-          acc[0][0][j][i] = fmaf(c, fq, acc[0][0][j][i]);
-          acc[1][0][j][i] = fmaf(c, fk, acc[1][0][j][i]);
-          gp[j][i] = ua * ga[i];
-          dot += gp[j][i] * xa;
+          vfma(gp[j], p[j], acc[kind][0][j], acc[kind][0][j]);
+          vmul(gp[j], ga, gp[j]);
+          vdot(gp[j], p[j], dots);
         }
-      }
-      const float m = group_sum(dot, a.lg) / (float)a.d;
-      if (!live || !xb) continue;
-      T* out = xb + node * a.ldxb + hd;
+        const float m = group_sum(dots.x + dots.y, a.lg) * a.inv_d;
+        if (live && xb) {
 #pragma unroll
-      for (int j = 0; j < NIT; ++j) {
-        if (u.at[j] < 0) continue;
-        float v[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = r * (gp[j][i] - p[j][i] * m);
-        store_pack<T, W>(out + u.at[j], v);
-        if (u.pair[j]) {
-#pragma unroll
-          for (int i = 0; i < W; ++i) v[i] = r * (gq[j][i] - q[j][i] * m);
-          store_pack<T, W>(out + u.at[j] + a.R, v);
+          for (int j = 0; j < NIT; ++j) {
+            if (u.at[j] < 0) continue;
+            float v[W];
+            vfmas(p[j], -m, gp[j], v);
+            vscale(v, r, v);
+            store_pack<T, W>(br + u.at[j], v);
+            if (u.pair[j]) {
+              vfmas(q[j], -m, gq[j], v);
+              vscale(v, r, v);
+              store_pack<T, W>(br + u.at[j] + a.R, v);
+            }
+          }
         }
+        br += move;
       }
     }
     if (want_pos) {
@@ -299,7 +457,7 @@ __global__ void __launch_bounds__(256, 2) head_norm_vjp_kernel(HeadArgs a, const
   }
   if (!a.gpart) return;
   // groups of a warp, then warps
-  for (int i = tid; i < 8 * 2 * a.d; i += 256) red[i] = 0.0f;
+  for (int i = tid; i < 16 * a.d; i += 256) red[i] = 0.0f;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 2; ++k)
@@ -363,6 +521,7 @@ static int check_heads(const fc_head_desc* d, int n) {
   return FC_OK;
 }
 
+// Widest unit, up to 16 bytes, that the pairs are a multiple of.
 static int unit_width(const fc_head_desc* d) {
   int w = d->dtype == FC_F32 ? 4 : 8;
   while (d->pairs % w) w >>= 1;
@@ -374,6 +533,7 @@ static int unit_width(const fc_head_desc* d) {
 static void head_geom(const fc_head_desc* d, int n, HeadArgs& a) {
   const int W = unit_width(d), H = d->heads_q + d->heads_k;
   a.n = n; a.hq = d->heads_q; a.hk = d->heads_k; a.d = d->head_dim; a.R = d->pairs; a.eps = d->eps;
+  a.inv_d = 1.0f / (float)d->head_dim;
   a.units = d->pairs / W + (d->head_dim - 2 * d->pairs) / W;
   a.lg = 0;
   while (a.lg < 5 && (1 << a.lg) < a.units) ++a.lg;
@@ -382,6 +542,9 @@ static void head_geom(const fc_head_desc* d, int n, HeadArgs& a) {
   while (2 * a.hs <= H && 2 * a.hs <= groups &&
          (a.hs < 32 >> a.lg || (long long)n * a.hs / groups < 2 * device_sm_count()))
     a.hs *= 2;
+  // not more than an eighth of the groups without a head, while 256 bytes stay together
+  const auto rounds = [&](int h) { return (h + a.hs - 1) / a.hs * a.hs; };
+  while (a.hs > 1 && rounds(d->heads_q) + rounds(d->heads_k) > H + H / 8 && (a.hs >> 1) << a.lg >= 16) a.hs >>= 1;
 }
 static long long head_blocks(const HeadArgs& a) {
   const int nodes = (256 >> a.lg) / a.hs;
@@ -408,30 +571,24 @@ static int run_vjp(const HeadArgs& a, const void* x, const void* g, void* xb, cu
 }
 
 // units of a lane: a head has at most 128 / W of them and 32 lanes
-#define FC_HEAD_DISPATCH(RUN, ...)                                                                       \
-  do {                                                                                                   \
-    const int w = unit_width(desc);                                                                      \
-    if (desc->dtype == FC_F32)                                                                           \
-      return w == 4   ? RUN<float, 4, 1>(__VA_ARGS__)                                                    \
-             : w == 2 ? RUN<float, 2, 2>(__VA_ARGS__)                                                    \
-                      : RUN<float, 1, 4>(__VA_ARGS__);                                                   \
-    if (desc->dtype == FC_BF16)                                                                          \
-      return w == 8   ? RUN<__nv_bfloat16, 8, 1>(__VA_ARGS__)                                            \
-             : w == 4 ? RUN<__nv_bfloat16, 4, 1>(__VA_ARGS__)                                            \
-             : w == 2 ? RUN<__nv_bfloat16, 2, 2>(__VA_ARGS__)                                            \
-                      : RUN<__nv_bfloat16, 1, 4>(__VA_ARGS__);                                           \
-    return w == 8   ? RUN<__half, 8, 1>(__VA_ARGS__)                                                     \
-           : w == 4 ? RUN<__half, 4, 1>(__VA_ARGS__)                                                     \
-           : w == 2 ? RUN<__half, 2, 2>(__VA_ARGS__)                                                     \
-                    : RUN<__half, 1, 4>(__VA_ARGS__);                                                    \
-  } while (0)
-
+template <class T>
 static int launch_fwd(const fc_head_desc* desc, const HeadArgs& a, const void* x, void* y, cudaStream_t s) {
-  FC_HEAD_DISPATCH(run_fwd, a, x, y, s);
+  switch (unit_width(desc)) {
+    case 8: return run_fwd<T, sizeof(T) == 2 ? 8 : 4, 1>(a, x, y, s);
+    case 4: return run_fwd<T, 4, 1>(a, x, y, s);
+    case 2: return run_fwd<T, 2, 2>(a, x, y, s);
+    default: return run_fwd<T, 1, 4>(a, x, y, s);
+  }
 }
+template <class T>
 static int launch_vjp(const fc_head_desc* desc, const HeadArgs& a, const void* x, const void* g, void* xb,
                       cudaStream_t s) {
-  FC_HEAD_DISPATCH(run_vjp, a, x, g, xb, s);
+  switch (unit_width(desc)) {
+    case 8: return run_vjp<T, sizeof(T) == 2 ? 8 : 4, 1>(a, x, g, xb, s);
+    case 4: return run_vjp<T, 4, 1>(a, x, g, xb, s);
+    case 2: return run_vjp<T, 2, 2>(a, x, g, xb, s);
+    default: return run_vjp<T, 1, 4>(a, x, g, xb, s);
+  }
 }
 
 static bool row_step(long long ld, int heads, int d) { return ld >= (long long)heads * d; }
@@ -457,7 +614,10 @@ int fc_head_norm_rotate(const fc_head_desc* desc, int n_nodes, const void* x, in
   HeadArgs a{};
   head_geom(desc, n_nodes, a);
   a.ldx = ldx; a.ldy = ldy; a.gq = gamma_q; a.gk = gamma_k; a.pos = pos; a.freq = freq;
-  return launch_fwd(desc, a, x, y, (cudaStream_t)stream);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (desc->dtype == FC_F32) return launch_fwd<float>(desc, a, x, y, s);
+  if (desc->dtype == FC_BF16) return launch_fwd<__nv_bfloat16>(desc, a, x, y, s);
+  return launch_fwd<__half>(desc, a, x, y, s);
 }
 
 size_t fc_head_norm_rotate_vjp_workspace_size(const fc_head_desc* desc, int n_nodes) {
@@ -502,7 +662,9 @@ int fc_head_norm_rotate_vjp(const fc_head_desc* desc, int n_nodes, const void* x
   if (!x_bar && !gamma && !(pos_bar && desc->pairs)) return FC_OK;
   a.ldx = ldx; a.ldg = ldg; a.ldxb = ldxb; a.gq = gamma_q; a.gk = gamma_k; a.pos = pos; a.freq = freq;
   a.pos_bar = pos_bar;
-  const int rc = launch_vjp(desc, a, x, g, x_bar, s);
+  const int rc = desc->dtype == FC_F32    ? launch_vjp<float>(desc, a, x, g, x_bar, s)
+                 : desc->dtype == FC_BF16 ? launch_vjp<__nv_bfloat16>(desc, a, x, g, x_bar, s)
+                                          : launch_vjp<__half>(desc, a, x, g, x_bar, s);
   if (rc != FC_OK || !gamma) return rc;
   head_gamma_kernel<<<(2 * D + 31) / 32, 1024, 0, s>>>(vjp_blocks(a), D, a.gpart, gamma_q_bar, gamma_k_bar);
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;

@@ -99,8 +99,15 @@ struct alignas(sizeof(T) * W) Pack {
 };
 template <class T, int W>
 __device__ __forceinline__ void load_pack(const T* p, float (&out)[W]) {
-  const Pack<T, W> a = *reinterpret_cast<const Pack<T, W>*>(p);
-  a.get(out);
+  constexpr int P = sizeof(T) * W > 16 ? 16 / (int)sizeof(T) : W;   // values of one load
+#pragma unroll
+  for (int i = 0; i < W; i += P) {
+    const Pack<T, P> a = *reinterpret_cast<const Pack<T, P>*>(p + i);
+    float v[P];
+    a.get(v);
+#pragma unroll
+    for (int k = 0; k < P; ++k) out[i + k] = v[k];
+  }
 }
 template <class T, int W>
 __device__ __forceinline__ void store_pack(T* p, const float (&in)[W]) {
