@@ -27,6 +27,8 @@ struct AttnArgs {
   float2* part_ml;      // forward: [splits][nr H] maximum and sum
   const float2* stat;   // gradient: [nr H] log-sum (base 2), delta
   float4* rowpart;      // gradient: [splits][nr H] position and slope sums
+  float4* rowmean;      // tcgen05 gradient: the same sums of the weights alone, and
+  float* rowrest;       // the row's sum of dt, which an exact delta makes 0
   float4* colpart;      // gradient: [kv_splits][KV][ns] position sums
   int kv_splits;        // parts of the receivers (key and value gradients)
   float *part_k, *part_v;   // [kv_splits][ns KV][D] partial rows
@@ -392,5 +394,6 @@ int attn_pad(int head_dim);
 int launch_attn_fwd_tc(int dtype, const AttnArgs& a, cudaStream_t s);
 // fc_attention_tc_vjp.cu: 16-bit types, at most 64 heads to a key head
 int launch_attn_vjp_tc(int dtype, bool kv, const AttnArgs& a, cudaStream_t s);
+int launch_attn_row_fix(const AttnArgs& a, float2* stat, cudaStream_t s);
 
 }  // namespace fc

@@ -8,7 +8,11 @@
 // accumulating products stay in tensor memory:
 //   query gradient         R = q, g; T = k, v:  q_bar += dS k
 //   key, value gradients   R = k, v; T = q, g:  k_bar += dS q,  v_bar += P g
-// The position and slope sums come from the FP32 values in registers.  The two
+// The position and slope sums come from the FP32 values in registers.  Delta as
+// it comes in is as exact as the forward's output, whose long sum the tensor
+// core truncates (8e-6 of a slope gradient at 2300 senders, 1.6e-5 at 8192); the
+// query gradient's kernel therefore sums dt and the weights' own position and
+// slope sums too, from which attn_row_fix_kernel takes the rest out.  The two
 // groups take the tiles in turn, so that one's arithmetic runs beside the
 // other's products.  The heads of a key head are rows of the stream tile
 // (64 / G receivers by G heads), so their sum needs no atomics.
@@ -42,13 +46,15 @@ struct RowGrad {
   float2 mul, cap2, px, py, pz, sl, nl, nd;   // negated: slope (base 2), log-sum, delta
   float cap_f;
   // P (KV) and dS of 64 columns as 16-bit pairs; sums: position x, y, z, slope (query gradient)
+  // (and, for the query gradient: the weights' sums of the same four, and the sum of dt)
+  static constexpr int kSums = KV ? 3 : 9;
   template <bool Easy, bool Flags>
-  __device__ __forceinline__ void tile(uint32_t st, const float* in, uint32_t (&w)[KV ? 2 : 1][32], float2 (&sum)[4],
-                                       float& big) const {
+  __device__ __forceinline__ void tile(uint32_t st, const float* in, uint32_t (&w)[KV ? 2 : 1][32],
+                                       float2 (&sum)[kSums], float& big) const {
     const TanhPoly poly(1.0f);
     float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] = pair(0.0f);
+    for (int i = 0; i < kSums; ++i) sum[i] = pair(0.0f);
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t rs[32], rp[32];
@@ -95,7 +101,15 @@ struct RowGrad {
           sum[0] = fma2(wt, dx, sum[0]);
           sum[1] = fma2(wt, dy, sum[1]);
           sum[2] = fma2(wt, dz, sum[2]);
-          if (!KV) sum[3] = fma2(dt, dist, sum[3]);
+          if constexpr (!KV) {
+            const float2 wp = mul2(p, inv);
+            sum[3] = fma2(dt, dist, sum[3]);
+            sum[4] = fma2(wp, dx, sum[4]);
+            sum[5] = fma2(wp, dy, sum[5]);
+            sum[6] = fma2(wp, dz, sum[6]);
+            sum[7] = fma2(p, dist, sum[7]);
+            sum[8] = add2(sum[8], dt);
+          }
         }
         const float2 ds = Cap ? mul2(dt, dc) : dt;
         w[0][16 * hf + e] = pack2<T>(ds.x, ds.y);
@@ -327,7 +341,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_vjp_tc_kernel(AttnArgs a, 
       grad.nl = pair(-st.x);
       grad.nd = pair(-st.y);
     }
-    float2 sum[4] = {pair(0.0f), pair(0.0f), pair(0.0f), pair(0.0f)};
+    constexpr int NS = RowGrad<T, Cap, Bias, KV>::kSums;
+    float2 sum[NS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) sum[n] = pair(0.0f);
     bool easy = true;   // the last tile's scores were in the polynomial's range
     for (int i = wg; i < nt; i += 2) {
       const int s = i % NST, b = i % NB;
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_vjp_tc_kernel(AttnArgs a, 
       const float* in = info(s);
       const bool flags = !KV && (a.mask || (t0 + i + 1) * (long long)kAtStep > shi - slo);
       uint32_t w[KV ? 2 : 1][32];
-      float2 add[4];
+      float2 add[NS];
       float big = 0.0f;
       bool ok = false;
       if (!Cap || easy) {
@@ -355,7 +372,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_vjp_tc_kernel(AttnArgs a, 
       }
       if (!ok) grad.template tile<false, true>(st, in, w, add, big);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) sum[n] = add2(sum[n], add[n]);
+      for (int n = 0; n < NS; ++n) sum[n] = add2(sum[n], add[n]);
       tc::tmem_st32(st + kAtStep, w[0]);
       if (KV) tc::tmem_st32(st, w[KV ? 1 : 0]);
       tc::tmem_wait_st();
@@ -367,23 +384,27 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_vjp_tc_kernel(AttnArgs a, 
     if (nt > 0 && !fail && !tc::bar_wait(&done[(nt - 1) % NB], ((nt - 1) / NB) & 1, lim)) fail = true;
     tc::fence_after_sync();
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    float4* mg = reinterpret_cast<float4*>(smem);
-    const float4 my = make_float4(sum[0].x + sum[0].y, sum[1].x + sum[1].y, sum[2].x + sum[2].y, sum[3].x + sum[3].y);
-    if (wg == 1) mg[row] = my;
+    float* mg = reinterpret_cast<float*>(smem);   // [NS][128]
+    if (wg == 1)
+#pragma unroll
+      for (int n = 0; n < NS; ++n) mg[n * kAtRows + row] = sum[n].x + sum[n].y;
     asm volatile("bar.sync 1, 256;" ::: "memory");
     if (wg == 0 && mine && !fail) {
-      const float4 o = mg[row];
-      const float4 t = make_float4(my.x + o.x, my.y + o.y, my.z + o.z, my.w + o.w);
-      if (KV) {
+      float t[NS];
+#pragma unroll
+      for (int n = 0; n < NS; ++n) t[n] = sum[n].x + sum[n].y + mg[n * kAtRows + row];
+      if constexpr (KV) {
         if (a.colpart) {   // the slopes went in as -slope log2(e); towards the receiver
           const float f = keep ? kLn2 : 0.0f;
           a.colpart[((long long)blockIdx.z * a.KV + kvh) * a.ns + vr] =
-              keep ? make_float4(f * t.x, f * t.y, f * t.z, 0.0f) : make_float4(0.f, 0.f, 0.f, 0.f);
+              keep ? make_float4(f * t[0], f * t[1], f * t[2], 0.0f) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
       } else if (a.rowpart) {
         const float sl = Bias ? -a.slope[head] : 0.0f;
-        a.rowpart[(long long)blockIdx.z * a.nr * a.H + node * a.H + head] =
-            make_float4(sl * t.x, sl * t.y, sl * t.z, -t.w);
+        const long long pr = (long long)blockIdx.z * a.nr * a.H + node * a.H + head;
+        a.rowpart[pr] = make_float4(sl * t[0], sl * t[1], sl * t[2], -t[3]);
+        a.rowmean[pr] = make_float4(sl * t[4], sl * t[5], sl * t[6], -t[7]);
+        a.rowrest[pr] = t[8];
       }
     }
     // accumulators: KV: one per group; else the groups take the 32-column blocks in turn
@@ -454,6 +475,30 @@ template <class T>
 static int run_dim(bool kv, const AttnArgs& a, cudaStream_t s) {
   if (a.D <= 64) return kv ? run_kind<T, 64, true>(a, s) : run_kind<T, 64, false>(a, s);
   return kv ? run_kind<T, 128, true>(a, s) : run_kind<T, 128, false>(a, s);
+}
+
+// Takes the rest of delta out of a row's sums, parts added: with e = sum dt (the
+// error of delta, as the weights sum to 1), the sums of P (dP - delta) x are
+// those of dt x less e times those of P x.  They go to the first part; delta
+// itself is put right for the sender side.
+__global__ void __launch_bounds__(256) attn_row_fix_kernel(AttnArgs a, float2* __restrict__ stat) {
+  const long long rows = (long long)a.nr * a.H, row = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (row >= rows) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f), m = s;
+  float e = 0.0f;
+  for (int p = 0; p < a.splits; ++p) {
+    const float4 x = a.rowpart[p * rows + row], y = a.rowmean[p * rows + row];
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    m.x += y.x; m.y += y.y; m.z += y.z; m.w += y.w;
+    e += a.rowrest[p * rows + row];
+  }
+  a.rowpart[row] = make_float4(s.x - e * m.x, s.y - e * m.y, s.z - e * m.z, s.w - e * m.w);
+  stat[row].y += e;
+}
+int launch_attn_row_fix(const AttnArgs& a, float2* stat, cudaStream_t s) {
+  const long long rows = (long long)a.nr * a.H;
+  attn_row_fix_kernel<<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(a, stat);
+  return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
 }
 
 int launch_attn_vjp_tc(int dtype, bool kv, const AttnArgs& a, cudaStream_t s) {

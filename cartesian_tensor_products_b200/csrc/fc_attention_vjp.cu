@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(256) attn_slope_kernel(AttnArgs a, float* __re
 
 struct VjpLayout {
   AttnPlan plan;
-  size_t stat, part, rowpart, colpart, part_k, part_v, bytes;
+  size_t stat, part, rowpart, rowmean, rowrest, colpart, part_k, part_v, bytes;
 };
 static VjpLayout vjp_layout(const fc_attn_desc* d, int B, int nr, int ns) {
   VjpLayout l;
@@ -431,7 +431,9 @@ static VjpLayout vjp_layout(const fc_attn_desc* d, int B, int nr, int ns) {
   const size_t pk = l.plan.kv_splits > 1 ? round16(cp * d->head_dim * sizeof(float)) : 0;
   l.stat = 0;
   l.rowpart = round16(rows * sizeof(float2));
-  l.colpart = l.rowpart + rp * sizeof(float4);
+  l.rowmean = l.rowpart + rp * sizeof(float4);
+  l.rowrest = l.rowmean + (l.plan.tc_vjp ? rp * sizeof(float4) : 0);
+  l.colpart = l.rowrest + (l.plan.tc_vjp ? round16(rp * sizeof(float)) : 0);
   l.part = l.colpart + cp * sizeof(float4);
   l.part_k = l.part + pq;
   l.part_v = l.part_k + pk;
@@ -477,8 +479,13 @@ static int run_vjp(int dtype, const AttnArgs& a, const VjpWants& w, bool tc, con
   const long long rows = (long long)a.nr * a.H, cols = (long long)a.ns * a.KV;
   int rc = FC_OK;
   if (a.nr > 0) attn_stat_kernel<T><<<blocks(rows, 32), 256, 0, s>>>(a, o32, a.lse, stat);
-  if (a.nr > 0 && (a.qb || w.pos_recv_bar || w.slope_bar)) {
+  AttnArgs sums = a;   // as the sums over heads and nodes see it
+  if (a.nr > 0 && (a.qb || a.rowpart)) {
     rc = run_side<T>(dtype, tc, false, a, s);
+    if (rc == FC_OK && tc && a.rowpart) {
+      rc = launch_attn_row_fix(a, stat, s);
+      sums.splits = 1;
+    }
     if (a.qb && a.splits > 1)
       attn_vjp_join_kernel<T><<<blocks(rows, 8), 256, 0, s>>>(rows, a.D, a.splits, a.part, static_cast<T*>(a.qb));
   }
@@ -493,10 +500,10 @@ static int run_vjp(int dtype, const AttnArgs& a, const VjpWants& w, bool tc, con
   }
   if (rc != FC_OK) return rc;
   if (w.pos_recv_bar && a.nr > 0)
-    attn_pos_kernel<<<blocks(a.nr, 8), 256, 0, s>>>(a, true, w.self, a.nr, w.pos_recv_bar);
+    attn_pos_kernel<<<blocks(a.nr, 8), 256, 0, s>>>(sums, true, w.self, a.nr, w.pos_recv_bar);
   if (w.pos_send_bar && a.ns > 0)
-    attn_pos_kernel<<<blocks(a.ns, 8), 256, 0, s>>>(a, false, true, a.ns, w.pos_send_bar);
-  if (w.slope_bar) attn_slope_kernel<<<a.H, 256, 0, s>>>(a, w.slope_bar);
+    attn_pos_kernel<<<blocks(a.ns, 8), 256, 0, s>>>(sums, false, true, a.ns, w.pos_send_bar);
+  if (w.slope_bar) attn_slope_kernel<<<a.H, 256, 0, s>>>(sums, w.slope_bar);
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
 }
 
@@ -566,12 +573,14 @@ int fc_node_attention_vjp(const fc_attn_desc* desc, int n_struct, int n_recv, in
   a.part_k = reinterpret_cast<float*>(ws + l.part_k);
   a.part_v = reinterpret_cast<float*>(ws + l.part_v);
   a.stat = stat;
-  a.rowpart = pos_recv_bar || slope_bar ? reinterpret_cast<float4*>(ws + l.rowpart) : nullptr;
+  // the tcgen05 kernels put delta right for the senders' position sums too
+  const bool tc = l.plan.tc_vjp && n_recv > 0 && n_send > 0;   // the tensor maps need rows on both sides
+  a.rowpart = pos_recv_bar || slope_bar || (tc && pos_send_bar) ? reinterpret_cast<float4*>(ws + l.rowpart) : nullptr;
+  a.rowmean = reinterpret_cast<float4*>(ws + l.rowmean);
+  a.rowrest = reinterpret_cast<float*>(ws + l.rowrest);
   a.colpart = pos_send_bar || (w.self && pos_recv_bar) ? reinterpret_cast<float4*>(ws + l.colpart) : nullptr;
   a.part = reinterpret_cast<float*>(ws + l.part);
   a.qb = q_bar; a.kb = k_bar; a.vb = v_bar;
-  // the tensor maps need rows on both sides
-  const bool tc = l.plan.tc_vjp && n_recv > 0 && n_send > 0;
   if (desc->dtype == FC_F32) return run_vjp<float>(FC_F32, a, w, false, out_f32, stat, s);
   if (desc->dtype == FC_BF16) return run_vjp<__nv_bfloat16>(FC_BF16, a, w, tc, out_f32, stat, s);
   return run_vjp<__half>(FC_F16, a, w, tc, out_f32, stat, s);
