@@ -19,6 +19,97 @@ struct FwdSmem {
   static constexpr size_t bytes = q + 4 * kv + 2 * BN * sizeof(float4);
 };
 
+// The two rows of a thread (lane/4 and 8 more of a strip) and their running state.
+struct StripRows {
+  float px[2], py[2], pz[2], sl[2], mul, cap2;
+  __device__ __forceinline__ StripRows(const AttnArgs& a, long long first, long long end, int kvh) {
+    const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const long long r = first + g + 8 * h < end ? first + g + 8 * h : end - 1;
+      px[h] = py[h] = pz[h] = sl[h] = 0.0f;
+      if (a.pos_r) {
+        const float* p = a.pos_r + 3 * (r / a.G);
+        px[h] = p[0]; py[h] = p[1]; pz[h] = p[2];
+        sl[h] = a.slope[kvh * a.G + r % a.G] * kLog2e;
+      }
+    }
+    mul = a.cap > 0.0f ? a.scale / a.cap : a.scale * kLog2e;
+    cap2 = a.cap * kLog2e;
+  }
+};
+template <int DP>
+struct StripState {
+  float acc[DP / 8][4], m[2], l[2];
+  __device__ __forceinline__ StripState() {
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[d][e] = 0.0f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.0f;
+  }
+};
+
+// One warp: 16 rows at q against 8 nl keys and values; in: position of each, w = 1 if not there.
+template <class T, int DP, int NT, bool Two>
+__device__ __forceinline__ void strip_step(const AttnArgs& a, const StripRows& r, StripState<DP>& state, const T* q,
+                                           const T* k, const T* v, const float4* in, int nl, bool ragged) {
+  const int c2 = 2 * (threadIdx.x & 3);
+  float s[NT][4];
+  strip_nt<T, DP, NT>(s, q, k, nl);
+  if (a.cap > 0.0f) strip_tanh<T, NT>(s, r.mul);
+  const float f = a.cap > 0.0f ? r.cap2 : r.mul;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[n][e] *= f;
+  if (a.pos_r) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float4 p = in[n * 8 + c2 + c];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float dx = r.px[h] - p.x, dy = r.py[h] - p.y, dz = r.pz[h] - p.z;
+          const float d2 = dx * dx + dy * dy + dz * dz;
+          s[n][2 * h + c] -= r.sl[h] * (d2 * rsq(d2 + kD2Seed));
+        }
+      }
+  }
+  if (ragged) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (in[n * 8 + c2 + c].w != 0.0f) s[n][c] = s[n][2 + c] = -INFINITY;
+  }
+  float alpha[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float mx = state.m[h];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * h], s[n][2 * h + 1]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    alpha[h] = ex2(state.m[h] - base);
+    state.m[h] = mx;
+    float sum = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float p = ex2(s[n][2 * h + c] - base);
+        s[n][2 * h + c] = p;
+        sum += p;
+      }
+    state.l[h] = state.l[h] * alpha[h] + sum;
+  }
+  strip_pn<T, DP, NT, Two>(state.acc, s, v, alpha[0], alpha[1], nl);
+}
+
 template <class T, int DP, bool Two>
 __global__ void __launch_bounds__(128) attn_fwd_kernel(AttnArgs a) {
   constexpr int BN = kStep<T, DP>, NT = BN / 8, S = kStride<T, DP>;
@@ -46,8 +137,9 @@ __global__ void __launch_bounds__(128) attn_fwd_kernel(AttnArgs a) {
   auto load_kv = [&](int t, int st) {
     const long long j0 = slo + (long long)t * BN;
     auto live = [&](int r) { return j0 + r < shi && (!a.mask || a.mask[j0 + r]); };
-    load_rows<T, DP, BN, 128>(ks + st * BN * S, a.D, tid, [&](int r) { return k + (j0 + r) * a.ldk; }, live);
-    load_rows<T, DP, BN, 128>(vs + st * BN * S, a.D, tid, [&](int r) { return v + (j0 + r) * a.ldv; }, live);
+    load_rows2<T, DP, BN, 128>(
+        ks + st * BN * S, vs + st * BN * S, a.D, tid, [&](int r) { return k + (j0 + r) * a.ldk; },
+        [&](int r) { return v + (j0 + r) * a.ldv; }, live);
     if (tid < BN) {
       float4 f = make_float4(0.f, 0.f, 0.f, live(tid) ? 0.f : 1.f);
       if (a.pos_r && live(tid)) {
@@ -60,119 +152,40 @@ __global__ void __launch_bounds__(128) attn_fwd_kernel(AttnArgs a) {
   if (t0 < t1) load_kv(t0, 0);
   cp_commit();
 
-  // the two rows of this thread
-  const int g = lane >> 2, c2 = 2 * (lane & 3);
-  long long vr[2];
-  float px[2], py[2], pz[2], sl[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    vr[h] = at.v0 + warp * 16 + g + 8 * h;
-    const long long r = vr[h] < at.v1 ? vr[h] : at.v0;
-    px[h] = py[h] = pz[h] = sl[h] = 0.0f;
-    if (a.pos_r) {
-      const float* p = a.pos_r + 3 * (r / a.G);
-      px[h] = p[0]; py[h] = p[1]; pz[h] = p[2];
-      sl[h] = a.slope[kvh * a.G + r % a.G] * kLog2e;
-    }
-  }
-  const float mul = a.cap > 0.0f ? a.scale / a.cap : a.scale * kLog2e;
-  const float cap2 = a.cap * kLog2e;
-  float acc[DP / 8][4];
-#pragma unroll
-  for (int d = 0; d < DP / 8; ++d)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[d][e] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-
-  const bool idle = at.v0 + warp * 16 >= at.v1;
+  StripRows rows(a, at.v0 + warp * 16, at.v1, kvh);
+  StripState<DP> state;
+  const bool idle = at.v0 + warp * 16 >= at.v1;   // none of the warp's rows is there
   for (int t = t0; t < t1; ++t) {
     const int st = (t - t0) & 1;
     if (t + 1 < t1) load_kv(t + 1, st ^ 1);
     cp_commit();
     cp_wait<1>();
     __syncthreads();
-    if (idle) {   // none of the warp's rows is there
-      __syncthreads();
-      continue;
+    if (!idle) {
+      const long long left = shi - slo - (long long)t * BN;
+      strip_step<T, DP, NT, Two>(a, rows, state, qs + warp * 16 * S, ks + st * BN * S, vs + st * BN * S, info + st * BN,
+                                 left >= BN ? NT : (int)(left + 7) / 8, a.mask || left < BN);
     }
-    const float4* in = info + st * BN;
-    float s[NT][4];
-    const long long left = shi - slo - (long long)t * BN;
-    const int nl = left >= BN ? NT : (int)(left + 7) / 8;   // column tiles that are there
-    strip_nt<T, DP, NT>(s, qs + warp * 16 * S, ks + st * BN * S, nl);
-    if (a.cap > 0.0f) {
-      strip_tanh<T, NT>(s, mul);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] *= cap2;
-    } else {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] *= mul;
-    }
-    if (a.pos_r) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float4 f = in[n * 8 + c2 + c];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float dx = px[h] - f.x, dy = py[h] - f.y, dz = pz[h] - f.z;
-            const float d2 = dx * dx + dy * dy + dz * dz;
-            s[n][2 * h + c] -= sl[h] * (d2 * rsq(d2 + kD2Seed));
-          }
-        }
-    }
-    const bool ragged = a.mask || slo + (long long)(t + 1) * BN > shi;
-    if (ragged) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (in[n * 8 + c2 + c].w != 0.0f) s[n][c] = s[n][2 + c] = -INFINITY;
-    }
-    float alpha[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float mx = m[h];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * h], s[n][2 * h + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float base = mx == -INFINITY ? 0.0f : mx;
-      alpha[h] = ex2(m[h] - base);
-      m[h] = mx;
-      float sum = 0.0f;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float p = ex2(s[n][2 * h + c] - base);
-          s[n][2 * h + c] = p;
-          sum += p;
-        }
-      l[h] = l[h] * alpha[h] + sum;
-    }
-    strip_pn<T, DP, NT, Two>(acc, s, vs + st * BN * S, alpha[0], alpha[1], nl);
     __syncthreads();
   }
   cp_wait<0>();
 
+  const int g = lane >> 2, c2 = 2 * (lane & 3);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float sum = l[h];
+    const long long vr = at.v0 + warp * 16 + g + 8 * h;
+    const float m = state.m[h];
+    const auto& acc = state.acc;
+    float sum = state.l[h];
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if (vr[h] >= at.v1) continue;
-    const long long node = vr[h] / a.G;
-    const int head = kvh * a.G + (int)(vr[h] % a.G);
+    if (vr >= at.v1) continue;
+    const long long node = vr / a.G;
+    const int head = kvh * a.G + (int)(vr % a.G);
     const long long row = node * a.H + head;
     if (a.splits > 1) {
       const long long pr = (long long)blockIdx.z * a.nr * a.H + row;
-      if ((lane & 3) == 0) a.part_ml[pr] = make_float2(m[h], sum);
+      if ((lane & 3) == 0) a.part_ml[pr] = make_float2(m, sum);
 #pragma unroll
       for (int d = 0; d < DP / 8; ++d)
         if (d * 8 < a.D)
@@ -180,7 +193,7 @@ __global__ void __launch_bounds__(128) attn_fwd_kernel(AttnArgs a) {
       continue;
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (a.lse && (lane & 3) == 0) a.lse[row] = (m[h] + log2f(sum)) * kLn2;
+    if (a.lse && (lane & 3) == 0) a.lse[row] = (m + log2f(sum)) * kLn2;
     T* o = static_cast<T*>(a.out) + node * a.ldo + (long long)head * a.D;
 #pragma unroll
     for (int d = 0; d < DP / 8; ++d) {
@@ -189,6 +202,133 @@ __global__ void __launch_bounds__(128) attn_fwd_kernel(AttnArgs a) {
       store_pack<T, 2>(o + d * 8 + c2, v2);
       if (a.o32) store_pack<float, 2>(a.o32 + row * a.D + d * 8 + c2, v2);
     }
+  }
+}
+
+// The same for few rows: a tile of 16 virtual rows, which all four warps hold,
+// each taking a quarter of every key tile with a running state of its own;
+// merged at the end.  With 64-row tiles three of four warps had no rows.
+template <class T, int DP>
+struct FewSmem {
+  static constexpr int BW = 16, BN = 4 * BW, S = kStride<T, DP>;
+  static constexpr size_t kv = sizeof(T) * BN * S, q = sizeof(T) * 16 * S;
+  static constexpr size_t merge = 4 * 16 * (DP + 2) * sizeof(float);   // over keys and values
+  static constexpr size_t bytes = q + 4 * kv + 2 * BN * sizeof(float4);
+  static_assert(merge <= 4 * kv && bytes <= 232448, "shared memory");
+};
+
+template <class T, int DP, bool Two>
+__global__ void __launch_bounds__(128) attn_few_kernel(AttnArgs a) {
+  using L = FewSmem<T, DP>;
+  constexpr int BN = L::BN, NT = L::BW / 8, S = kStride<T, DP>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  T* qs = reinterpret_cast<T*>(smem);
+  T* ks = qs + 16 * S;             // two stages
+  T* vs = ks + 2 * BN * S;
+  float4* info = reinterpret_cast<float4*>(vs + 2 * BN * S);   // [2][BN]: sender position, w = 1 if not there
+  TileAt at;
+  if (!find_tile(a.recv_ptr, a.B, a.nr, a.G, 16, blockIdx.x, at)) return;
+  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int slo, shi;
+  other_side(a.send_ptr, a.B, a.ns, at.b, slo, shi);
+  const int all = shi > slo ? (shi - slo + BN - 1) / BN : 0;
+  const int t0 = (int)((long long)all * blockIdx.z / a.splits), t1 = (int)((long long)all * (blockIdx.z + 1) / a.splits);
+  const T* q = static_cast<const T*>(a.q);
+  const T* k = static_cast<const T*>(a.k) + (long long)kvh * a.D;
+  const T* v = static_cast<const T*>(a.v) + (long long)kvh * a.D;
+  auto qrow = [&](int r) {
+    const long long vr = at.v0 + r < at.v1 ? at.v0 + r : at.v0;
+    return q + vr / a.G * a.ldq + (kvh * a.G + vr % a.G) * (long long)a.D;
+  };
+  load_rows<T, DP, 16, 128>(qs, a.D, tid, qrow, [&](int r) { return at.v0 + r < at.v1; });
+  auto load_kv = [&](int t, int st) {
+    const long long j0 = slo + (long long)t * BN;
+    auto live = [&](int r) { return j0 + r < shi && (!a.mask || a.mask[j0 + r]); };
+    load_rows2<T, DP, BN, 128>(
+        ks + st * BN * S, vs + st * BN * S, a.D, tid, [&](int r) { return k + (j0 + r) * a.ldk; },
+        [&](int r) { return v + (j0 + r) * a.ldv; }, live);
+    for (int r = tid; r < BN; r += 128) {
+      float4 f = make_float4(0.f, 0.f, 0.f, live(r) ? 0.f : 1.f);
+      if (a.pos_r && live(r)) {
+        const float* p = a.pos_s + 3 * (j0 + r);
+        f.x = p[0]; f.y = p[1]; f.z = p[2];
+      }
+      info[st * BN + r] = f;
+    }
+  };
+  if (t0 < t1) load_kv(t0, 0);
+  cp_commit();
+
+  StripRows rows(a, at.v0, at.v1, kvh);
+  StripState<DP> state;
+  for (int t = t0; t < t1; ++t) {
+    const int st = (t - t0) & 1;
+    if (t + 1 < t1) load_kv(t + 1, st ^ 1);
+    cp_commit();
+    cp_wait<1>();
+    __syncthreads();
+    const int b = st * BN + warp * L::BW;
+    const long long left = shi - slo - (long long)t * BN - warp * L::BW;
+    const int nl = left >= L::BW ? NT : left <= 0 ? 0 : (int)(left + 7) / 8;
+    if (nl > 0)
+      strip_step<T, DP, NT, Two>(a, rows, state, qs, ks + b * S, vs + b * S, info + b, nl, a.mask || left < L::BW);
+    __syncthreads();
+  }
+  cp_wait<0>();
+
+  // merge: [warp][16 rows] of DP values, maximum and sum
+  float* mg = reinterpret_cast<float*>(ks);
+  constexpr int MS = DP + 2;
+  const int g = lane >> 2, c2 = 2 * (lane & 3);
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float sum = state.l[h];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    float* to = mg + (warp * 16 + g + 8 * h) * MS;
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) {
+      to[d * 8 + c2] = state.acc[d][2 * h];
+      to[d * 8 + c2 + 1] = state.acc[d][2 * h + 1];
+    }
+    if ((lane & 3) == 0) {
+      to[DP] = state.m[h];
+      to[DP + 1] = sum;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < 16 * (a.D / 4); i += 128) {
+    const int r = i / (a.D / 4), c = (i - r * (a.D / 4)) * 4;
+    const long long vr = at.v0 + r;
+    if (vr >= at.v1) break;
+    float m = -INFINITY, sum = 0.0f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, mg[(w * 16 + r) * MS + DP]);
+    const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float* f = mg + (w * 16 + r) * MS;
+      const float e = ex2(f[DP] - base);
+      sum += e * f[DP + 1];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) x[n] += e * f[c + n];
+    }
+    const long long node = vr / a.G;
+    const int head = kvh * a.G + (int)(vr % a.G);
+    const long long row = node * a.H + head;
+    if (a.splits > 1) {
+      const long long pr = (long long)blockIdx.z * a.nr * a.H + row;
+      if (c == 0) a.part_ml[pr] = make_float2(m, sum);
+      store_pack<float, 4>(a.part + pr * a.D + c, x);
+      continue;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (a.lse && c == 0) a.lse[row] = (m + log2f(sum)) * kLn2;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) x[n] *= inv;
+    store_pack<T, 4>(static_cast<T*>(a.out) + node * a.ldo + (long long)head * a.D + c, x);
+    if (a.o32) store_pack<float, 4>(a.o32 + row * a.D + c, x);
   }
 }
 
@@ -208,6 +348,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a) {
   const float base = m == -INFINITY ? 0.0f : m;
   float sum = 0.0f, acc[4] = {0.f, 0.f, 0.f, 0.f};
   const int c = lane * 4;
+#pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
     const float2 ml = a.part_ml[s * step + row];
     const float w = ex2(ml.x - base);
@@ -260,16 +401,28 @@ AttnPlan attn_plan(const fc_attn_desc* d, int B, int nr, int ns) {
   const int step = d->dtype == FC_F32 && d->head_dim > 64 ? 32 : 64;
   p.tc = d->dtype != FC_F32 && per_r >= FC_TC_ROWS && per_s >= 128 && rows < (1ll << 31);
   p.tc_vjp = p.tc && G <= 64;
-  p.splits = p.tc ? parts((rows + 127) / 128 * KV, sms, per_s, 64) : parts((rows + 63) / 64 * KV, 2 * sms, per_s, step);
-  p.q_splits = p.tc_vjp ? parts((rows + 127) / 128 * KV, sms, per_s, 64)
-                        : parts((rows + 63) / 64 * KV, 2 * sms, per_s, step);
-  p.kv_splits = p.tc_vjp ? parts(((long long)ns + 127) / 128 * KV, sms, per_r, 64)
-                         : parts(((long long)ns + 63) / 64 * KV, 2 * sms, per_r, step);
+  // few: up to two 16-row tiles a structure
+  p.few = !p.tc && per_r <= 32;
+  const auto tiles = [&](long long n, int tile) { return (n + tile - 1) / tile > B ? (n + tile - 1) / tile : B; };
+  p.splits = p.tc    ? parts(tiles(rows, 128) * KV, sms, per_s, 64)
+             : p.few ? parts(tiles(rows, 16) * KV, 4 * sms, per_s, 64)
+                     : parts(tiles(rows, 64) * KV, 2 * sms, per_s, step);
+  p.q_splits = p.tc_vjp ? parts(tiles(rows, 128) * KV, sms, per_s, 64)
+                        : parts(tiles(rows, 64) * KV, 2 * sms, per_s, step);
+  p.kv_splits = p.tc_vjp ? parts(tiles(ns, 128) * KV, sms, per_r, 64)
+                         : parts(tiles(ns, 64) * KV, 2 * sms, per_r, step);
   return p;
 }
 
 template <class T, int DP, bool Two>
-static int run_attn(const AttnArgs& a, cudaStream_t s) {
+static int run_attn(bool few, const AttnArgs& a, cudaStream_t s) {
+  if (few) {
+    static DeviceFlags few_ready;
+    constexpr size_t bytes = FewSmem<T, DP>::bytes;
+    if (set_smem_once(few_ready, attn_few_kernel<T, DP, Two>, bytes) != FC_OK) return FC_ERR_CUDA;
+    attn_few_kernel<T, DP, Two><<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, 16), a.KV, a.splits), 128, bytes, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
+  }
   static DeviceFlags ready;
   constexpr size_t bytes = FwdSmem<T, DP>::bytes;
   if (set_smem_once(ready, attn_fwd_kernel<T, DP, Two>, bytes) != FC_OK) return FC_ERR_CUDA;
@@ -278,19 +431,19 @@ static int run_attn(const AttnArgs& a, cudaStream_t s) {
 }
 
 template <class T>
-static int run_strips(const AttnArgs& a, cudaStream_t s) {
+static int run_strips(bool few, const AttnArgs& a, cudaStream_t s) {
   const bool two = sizeof(T) == 2 && a.o32;
   switch (attn_pad(a.D)) {
-    case 16: return two ? run_attn<T, 16, sizeof(T) == 2>(a, s) : run_attn<T, 16, false>(a, s);
-    case 32: return two ? run_attn<T, 32, sizeof(T) == 2>(a, s) : run_attn<T, 32, false>(a, s);
-    case 64: return two ? run_attn<T, 64, sizeof(T) == 2>(a, s) : run_attn<T, 64, false>(a, s);
-    default: return two ? run_attn<T, 128, sizeof(T) == 2>(a, s) : run_attn<T, 128, false>(a, s);
+    case 16: return two ? run_attn<T, 16, sizeof(T) == 2>(few, a, s) : run_attn<T, 16, false>(few, a, s);
+    case 32: return two ? run_attn<T, 32, sizeof(T) == 2>(few, a, s) : run_attn<T, 32, false>(few, a, s);
+    case 64: return two ? run_attn<T, 64, sizeof(T) == 2>(few, a, s) : run_attn<T, 64, false>(few, a, s);
+    default: return two ? run_attn<T, 128, sizeof(T) == 2>(few, a, s) : run_attn<T, 128, false>(few, a, s);
   }
 }
 
 template <class T>
-static int run_attn_type(int dtype, bool tc, const AttnArgs& a, cudaStream_t s) {
-  const int rc = tc ? launch_attn_fwd_tc(dtype, a, s) : run_strips<T>(a, s);
+static int run_attn_type(int dtype, const AttnPlan& plan, const AttnArgs& a, cudaStream_t s) {
+  const int rc = plan.tc && a.ns > 0 ? launch_attn_fwd_tc(dtype, a, s) : run_strips<T>(plan.few, a, s);
   if (rc != FC_OK || a.splits == 1) return rc;
   attn_join_kernel<T><<<(unsigned)(((long long)a.nr * a.H + 7) / 8), 256, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
@@ -337,7 +490,7 @@ int fc_node_attention(const fc_attn_desc* desc, int n_struct, int n_recv, int n_
   a.out = out; a.lse = lse; a.o32 = out_f32;
   const AttnPlan plan = attn_plan(desc, n_struct, n_recv, n_send);
   a.splits = plan.splits;
-  if (tile_slots(a.B, a.nr, a.G, 64) > INT32_MAX) return FC_ERR_ARG;
+  if (tile_slots(a.B, a.nr, a.G, 16) > INT32_MAX) return FC_ERR_ARG;
   if (a.splits > 1) {
     const size_t need = fc_node_attention_workspace_size(desc, n_struct, n_recv, n_send);
     if (!workspace || ws_bytes < need) return FC_ERR_WORKSPACE;
@@ -347,9 +500,9 @@ int fc_node_attention(const fc_attn_desc* desc, int n_struct, int n_recv, int n_
                                           round16((size_t)a.splits * n_recv * H * D * sizeof(float)));
   }
   cudaStream_t s = (cudaStream_t)stream;
-  if (desc->dtype == FC_F32) return run_attn_type<float>(FC_F32, false, a, s);
-  if (desc->dtype == FC_BF16) return run_attn_type<__nv_bfloat16>(FC_BF16, plan.tc, a, s);
-  return run_attn_type<__half>(FC_F16, plan.tc, a, s);
+  if (desc->dtype == FC_F32) return run_attn_type<float>(FC_F32, plan, a, s);
+  if (desc->dtype == FC_BF16) return run_attn_type<__nv_bfloat16>(FC_BF16, plan, a, s);
+  return run_attn_type<__half>(FC_F16, plan, a, s);
 }
 
 }  // extern "C"

@@ -189,6 +189,31 @@ __device__ __forceinline__ void load_rows(T* tile, int D, int tid, Src src, Live
   }
 }
 
+// The same for two arrays that share `live` (keys and values): its loads go out
+// together, ahead of the copies they decide on.
+template <class T, int DP, int ROWS, int THREADS, class Src1, class Src2, class Live>
+__device__ __forceinline__ void load_rows2(T* tile1, T* tile2, int D, int tid, Src1 src1, Src2 src2, Live live) {
+  constexpr int VEC = 16 / sizeof(T), CH = DP / VEC, U = 8;
+  static_assert(ROWS * CH % THREADS == 0, "whole rounds");
+#pragma unroll 1
+  for (int i0 = tid; i0 < ROWS * CH; i0 += U * THREADS) {
+    bool ok[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * THREADS, r = i / CH;
+      ok[u] = i < ROWS * CH && (i - r * CH) * VEC < D && live(r);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * THREADS;
+      if (i >= ROWS * CH) break;
+      const int r = i / CH, c = (i - r * CH) * VEC;
+      cp16(tile1 + r * kStride<T, DP> + c, src1(ok[u] ? r : 0) + (ok[u] ? c : 0), ok[u]);
+      cp16(tile2 + r * kStride<T, DP> + c, src2(ok[u] ? r : 0) + (ok[u] ? c : 0), ok[u]);
+    }
+  }
+}
+
 // ----------------------------------------------------------------- products
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void* p) {
@@ -384,7 +409,7 @@ constexpr int kStep = sizeof(T) == 4 && DP > 64 ? 32 : 64;
 // kernels, and in how many parts of the senders (forward, query gradient) or
 // of the receivers (key and value gradients).
 struct AttnPlan {
-  bool tc, tc_vjp;
+  bool tc, few, tc_vjp;
   int splits, q_splits, kv_splits;
 };
 int check_attn(const fc_attn_desc* d, int n_struct, int n_recv, int n_send);

@@ -75,8 +75,9 @@ __global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
   auto load_kv = [&](int t, int st) {
     const long long j0 = slo + (long long)t * BN;
     auto live = [&](int r) { return j0 + r < shi && (!a.mask || a.mask[j0 + r]); };
-    load_rows<T, DP, BN, 128>(ks + st * BN * S, a.D, tid, [&](int r) { return k + (j0 + r) * a.ldk; }, live);
-    load_rows<T, DP, BN, 128>(vs + st * BN * S, a.D, tid, [&](int r) { return v + (j0 + r) * a.ldv; }, live);
+    load_rows2<T, DP, BN, 128>(
+        ks + st * BN * S, vs + st * BN * S, a.D, tid, [&](int r) { return k + (j0 + r) * a.ldk; },
+        [&](int r) { return v + (j0 + r) * a.ldv; }, live);
     if (tid < BN) {
       float4 f = make_float4(0.f, 0.f, 0.f, live(tid) ? 0.f : 1.f);
       if (a.pos_r && live(tid)) {

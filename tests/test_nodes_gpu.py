@@ -263,6 +263,10 @@ ATTN = {
     "all hidden": dict(recv=[9, 66], send=None, h=2, kv=1, d=16, dtype=F32, hide=1.1),
     "probe split": dict(recv=[1, 1], send=[3000, 2100], h=4, kv=2, d=64, dtype=F32, cap=3.0, hide=0.1),
     "probe split bf16": dict(recv=[2, 1, 1], send=[4000, 0, 1500], h=8, kv=2, d=128, dtype=BF16),
+    "few rows": dict(recv=[3, 20, 0, 9], send=[130, 40, 5, 700], h=6, kv=3, d=40, dtype=F32, cap=9.0, hide=0.2),
+    "few rows wide": dict(recv=[5, 1], send=[300, 65], h=8, kv=2, d=128, dtype=F32),
+    "few rows f16": dict(recv=[7, 1, 2], send=[1, 129, 33], h=4, kv=1, d=16, dtype=F16, bias=False),
+    "few rows, all hidden": dict(recv=[7, 1], send=[50, 129], h=4, kv=1, d=64, dtype=BF16, hide=1.1),
     "long": dict(recv=[1100], send=None, h=2, kv=1, d=64, dtype=F16, cap=3.0),
     "long f32": dict(recv=[1100], send=None, h=2, kv=2, d=64, dtype=F32),
     # enough blocks that the senders are not split: more tiles than a block has stages
