@@ -1,22 +1,27 @@
-// Node attention, forward.
+// Node attention, forward: entry point, plan and the strip kernel.
 //
-// One block takes 64 virtual rows (receivers x heads of a key head) of one
+// A block takes 16 WM virtual rows (receivers x heads of a key head) of one
 // structure and walks over its senders with a running maximum and sum: scores,
 // cap, distance bias and mask stay in registers, keys and values pass through
-// a double-buffered shared tile.  With few rows the senders are split over
-// blocks whose partial rows a second kernel joins.
+// a double-buffered shared tile.  A warp holds 16 of the rows and one of WN
+// parts of every key tile, with a running state of its own; the parts are
+// merged at the end.  WM = 4, WN = 1 or 2 in general; WM = 1, WN = 4 where a
+// structure has few rows (three of four warps had none).  With few blocks the
+// senders are split over blocks, whose partial rows a second kernel joins.
 #include <math.h>
 
 #include "fc_attention.cuh"
 
 namespace fc {
 
-template <class T, int DP>
-struct FwdSmem {
-  static constexpr int BN = kStep<T, DP>, S = kStride<T, DP>;
-  static constexpr size_t kv = sizeof(T) * BN * S;
-  static constexpr size_t q = sizeof(T) * 64 * S;
+template <class T, int DP, int WM, int WN>
+struct StripSmem {
+  static constexpr int BW = WM == 1 || (sizeof(T) == 4 && DP > 64) ? 16 : 32;   // a warp's part of a key tile
+  static constexpr int ROWS = 16 * WM, BN = WN * BW, S = kStride<T, DP>, threads = 32 * WM * WN;
+  static constexpr size_t kv = sizeof(T) * BN * S, q = sizeof(T) * ROWS * S;
+  static constexpr size_t merge = WN * ROWS * (DP + 2) * sizeof(float);   // over keys and values
   static constexpr size_t bytes = q + 4 * kv + 2 * BN * sizeof(float4);
+  static_assert(merge <= 4 * kv && bytes <= 232448, "shared memory");
 };
 
 // The two rows of a thread (lane/4 and 8 more of a strip) and their running state.
@@ -110,125 +115,18 @@ __device__ __forceinline__ void strip_step(const AttnArgs& a, const StripRows& r
   strip_pn<T, DP, NT, Two>(state.acc, s, v, alpha[0], alpha[1], nl);
 }
 
-template <class T, int DP, bool Two>
-__global__ void __launch_bounds__(128) attn_fwd_kernel(AttnArgs a) {
-  constexpr int BN = kStep<T, DP>, NT = BN / 8, S = kStride<T, DP>;
+template <class T, int DP, bool Two, int WM, int WN>
+__global__ void __launch_bounds__(32 * WM * WN) attn_strip_kernel(AttnArgs a) {
+  using L = StripSmem<T, DP, WM, WN>;
+  constexpr int BN = L::BN, NT = L::BW / 8, S = kStride<T, DP>, ROWS = L::ROWS, TH = L::threads;
   extern __shared__ __align__(16) unsigned char smem[];
   T* qs = reinterpret_cast<T*>(smem);
-  T* ks = qs + 64 * S;             // two stages
+  T* ks = qs + ROWS * S;           // two stages
   T* vs = ks + 2 * BN * S;
   float4* info = reinterpret_cast<float4*>(vs + 2 * BN * S);   // [2][BN]: sender position, w = 1 if not there
   TileAt at;
-  if (!find_tile(a.recv_ptr, a.B, a.nr, a.G, 64, blockIdx.x, at)) return;
-  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int slo, shi;
-  other_side(a.send_ptr, a.B, a.ns, at.b, slo, shi);
-  const int all = shi > slo ? (shi - slo + BN - 1) / BN : 0;
-  const int t0 = (int)((long long)all * blockIdx.z / a.splits), t1 = (int)((long long)all * (blockIdx.z + 1) / a.splits);
-
-  const T* q = static_cast<const T*>(a.q);
-  const T* k = static_cast<const T*>(a.k) + (long long)kvh * a.D;
-  const T* v = static_cast<const T*>(a.v) + (long long)kvh * a.D;
-  auto qrow = [&](int r) {
-    const long long vr = at.v0 + r < at.v1 ? at.v0 + r : at.v0;
-    return q + vr / a.G * a.ldq + (kvh * a.G + vr % a.G) * (long long)a.D;
-  };
-  load_rows<T, DP, 64, 128>(qs, a.D, tid, qrow, [&](int r) { return at.v0 + r < at.v1; });
-  auto load_kv = [&](int t, int st) {
-    const long long j0 = slo + (long long)t * BN;
-    auto live = [&](int r) { return j0 + r < shi && (!a.mask || a.mask[j0 + r]); };
-    load_rows2<T, DP, BN, 128>(
-        ks + st * BN * S, vs + st * BN * S, a.D, tid, [&](int r) { return k + (j0 + r) * a.ldk; },
-        [&](int r) { return v + (j0 + r) * a.ldv; }, live);
-    if (tid < BN) {
-      float4 f = make_float4(0.f, 0.f, 0.f, live(tid) ? 0.f : 1.f);
-      if (a.pos_r && live(tid)) {
-        const float* p = a.pos_s + 3 * (j0 + tid);
-        f.x = p[0]; f.y = p[1]; f.z = p[2];
-      }
-      info[st * BN + tid] = f;
-    }
-  };
-  if (t0 < t1) load_kv(t0, 0);
-  cp_commit();
-
-  StripRows rows(a, at.v0 + warp * 16, at.v1, kvh);
-  StripState<DP> state;
-  const bool idle = at.v0 + warp * 16 >= at.v1;   // none of the warp's rows is there
-  for (int t = t0; t < t1; ++t) {
-    const int st = (t - t0) & 1;
-    if (t + 1 < t1) load_kv(t + 1, st ^ 1);
-    cp_commit();
-    cp_wait<1>();
-    __syncthreads();
-    if (!idle) {
-      const long long left = shi - slo - (long long)t * BN;
-      strip_step<T, DP, NT, Two>(a, rows, state, qs + warp * 16 * S, ks + st * BN * S, vs + st * BN * S, info + st * BN,
-                                 left >= BN ? NT : (int)(left + 7) / 8, a.mask || left < BN);
-    }
-    __syncthreads();
-  }
-  cp_wait<0>();
-
-  const int g = lane >> 2, c2 = 2 * (lane & 3);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const long long vr = at.v0 + warp * 16 + g + 8 * h;
-    const float m = state.m[h];
-    const auto& acc = state.acc;
-    float sum = state.l[h];
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if (vr >= at.v1) continue;
-    const long long node = vr / a.G;
-    const int head = kvh * a.G + (int)(vr % a.G);
-    const long long row = node * a.H + head;
-    if (a.splits > 1) {
-      const long long pr = (long long)blockIdx.z * a.nr * a.H + row;
-      if ((lane & 3) == 0) a.part_ml[pr] = make_float2(m, sum);
-#pragma unroll
-      for (int d = 0; d < DP / 8; ++d)
-        if (d * 8 < a.D)
-          *reinterpret_cast<float2*>(a.part + pr * a.D + d * 8 + c2) = make_float2(acc[d][2 * h], acc[d][2 * h + 1]);
-      continue;
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (a.lse && (lane & 3) == 0) a.lse[row] = (m + log2f(sum)) * kLn2;
-    T* o = static_cast<T*>(a.out) + node * a.ldo + (long long)head * a.D;
-#pragma unroll
-    for (int d = 0; d < DP / 8; ++d) {
-      if (d * 8 >= a.D) continue;
-      const float v2[2] = {acc[d][2 * h] * inv, acc[d][2 * h + 1] * inv};
-      store_pack<T, 2>(o + d * 8 + c2, v2);
-      if (a.o32) store_pack<float, 2>(a.o32 + row * a.D + d * 8 + c2, v2);
-    }
-  }
-}
-
-// The same for few rows: a tile of 16 virtual rows, which all four warps hold,
-// each taking a quarter of every key tile with a running state of its own;
-// merged at the end.  With 64-row tiles three of four warps had no rows.
-template <class T, int DP>
-struct FewSmem {
-  static constexpr int BW = 16, BN = 4 * BW, S = kStride<T, DP>;
-  static constexpr size_t kv = sizeof(T) * BN * S, q = sizeof(T) * 16 * S;
-  static constexpr size_t merge = 4 * 16 * (DP + 2) * sizeof(float);   // over keys and values
-  static constexpr size_t bytes = q + 4 * kv + 2 * BN * sizeof(float4);
-  static_assert(merge <= 4 * kv && bytes <= 232448, "shared memory");
-};
-
-template <class T, int DP, bool Two>
-__global__ void __launch_bounds__(128) attn_few_kernel(AttnArgs a) {
-  using L = FewSmem<T, DP>;
-  constexpr int BN = L::BN, NT = L::BW / 8, S = kStride<T, DP>;
-  extern __shared__ __align__(16) unsigned char smem[];
-  T* qs = reinterpret_cast<T*>(smem);
-  T* ks = qs + 16 * S;             // two stages
-  T* vs = ks + 2 * BN * S;
-  float4* info = reinterpret_cast<float4*>(vs + 2 * BN * S);   // [2][BN]: sender position, w = 1 if not there
-  TileAt at;
-  if (!find_tile(a.recv_ptr, a.B, a.nr, a.G, 16, blockIdx.x, at)) return;
-  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (!find_tile(a.recv_ptr, a.B, a.nr, a.G, ROWS, blockIdx.x, at)) return;
+  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, wm = (tid >> 5) % WM, wn = (tid >> 5) / WM;
   int slo, shi;
   other_side(a.send_ptr, a.B, a.ns, at.b, slo, shi);
   const int all = shi > slo ? (shi - slo + BN - 1) / BN : 0;
@@ -240,14 +138,14 @@ __global__ void __launch_bounds__(128) attn_few_kernel(AttnArgs a) {
     const long long vr = at.v0 + r < at.v1 ? at.v0 + r : at.v0;
     return q + vr / a.G * a.ldq + (kvh * a.G + vr % a.G) * (long long)a.D;
   };
-  load_rows<T, DP, 16, 128>(qs, a.D, tid, qrow, [&](int r) { return at.v0 + r < at.v1; });
+  load_rows<T, DP, ROWS, TH>(qs, a.D, tid, qrow, [&](int r) { return at.v0 + r < at.v1; });
   auto load_kv = [&](int t, int st) {
     const long long j0 = slo + (long long)t * BN;
     auto live = [&](int r) { return j0 + r < shi && (!a.mask || a.mask[j0 + r]); };
-    load_rows2<T, DP, BN, 128>(
+    load_rows2<T, DP, BN, TH>(
         ks + st * BN * S, vs + st * BN * S, a.D, tid, [&](int r) { return k + (j0 + r) * a.ldk; },
         [&](int r) { return v + (j0 + r) * a.ldv; }, live);
-    for (int r = tid; r < BN; r += 128) {
+    for (int r = tid; r < BN; r += TH) {
       float4 f = make_float4(0.f, 0.f, 0.f, live(r) ? 0.f : 1.f);
       if (a.pos_r && live(r)) {
         const float* p = a.pos_s + 3 * (j0 + r);
@@ -259,24 +157,25 @@ __global__ void __launch_bounds__(128) attn_few_kernel(AttnArgs a) {
   if (t0 < t1) load_kv(t0, 0);
   cp_commit();
 
-  StripRows rows(a, at.v0, at.v1, kvh);
+  StripRows rows(a, at.v0 + wm * 16, at.v1, kvh);
   StripState<DP> state;
+  const bool idle = at.v0 + wm * 16 >= at.v1;   // none of the warp's rows is there
   for (int t = t0; t < t1; ++t) {
     const int st = (t - t0) & 1;
     if (t + 1 < t1) load_kv(t + 1, st ^ 1);
     cp_commit();
     cp_wait<1>();
     __syncthreads();
-    const int b = st * BN + warp * L::BW;
-    const long long left = shi - slo - (long long)t * BN - warp * L::BW;
-    const int nl = left >= L::BW ? NT : left <= 0 ? 0 : (int)(left + 7) / 8;
+    const int b = st * BN + wn * L::BW;
+    const long long left = shi - slo - (long long)t * BN - wn * L::BW;
+    const int nl = idle || left <= 0 ? 0 : left >= L::BW ? NT : (int)(left + 7) / 8;
     if (nl > 0)
-      strip_step<T, DP, NT, Two>(a, rows, state, qs, ks + b * S, vs + b * S, info + b, nl, a.mask || left < L::BW);
+      strip_step<T, DP, NT, Two>(a, rows, state, qs + wm * 16 * S, ks + b * S, vs + b * S, info + b, nl, a.mask || left < L::BW);
     __syncthreads();
   }
   cp_wait<0>();
 
-  // merge: [warp][16 rows] of DP values, maximum and sum
+  // merge: [part][rows] of DP values, maximum and sum
   float* mg = reinterpret_cast<float*>(ks);
   constexpr int MS = DP + 2;
   const int g = lane >> 2, c2 = 2 * (lane & 3);
@@ -286,7 +185,7 @@ __global__ void __launch_bounds__(128) attn_few_kernel(AttnArgs a) {
     float sum = state.l[h];
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    float* to = mg + (warp * 16 + g + 8 * h) * MS;
+    float* to = mg + (wn * ROWS + wm * 16 + g + 8 * h) * MS;
 #pragma unroll
     for (int d = 0; d < DP / 8; ++d) {
       to[d * 8 + c2] = state.acc[d][2 * h];
@@ -298,17 +197,18 @@ __global__ void __launch_bounds__(128) attn_few_kernel(AttnArgs a) {
     }
   }
   __syncthreads();
-  for (int i = tid; i < 16 * (a.D / 4); i += 128) {
-    const int r = i / (a.D / 4), c = (i - r * (a.D / 4)) * 4;
+  const int quads = a.D / 4;
+  for (int i = tid; i < ROWS * quads; i += TH) {
+    const int r = i / quads, c = (i - r * quads) * 4;
     const long long vr = at.v0 + r;
     if (vr >= at.v1) break;
     float m = -INFINITY, sum = 0.0f, x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) m = fmaxf(m, mg[(w * 16 + r) * MS + DP]);
+    for (int w = 0; w < WN; ++w) m = fmaxf(m, mg[(w * ROWS + r) * MS + DP]);
     const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float* f = mg + (w * 16 + r) * MS;
+    for (int w = 0; w < WN; ++w) {
+      const float* f = mg + (w * ROWS + r) * MS;
       const float e = ex2(f[DP] - base);
       sum += e * f[DP + 1];
 #pragma unroll
@@ -414,20 +314,21 @@ AttnPlan attn_plan(const fc_attn_desc* d, int B, int nr, int ns) {
   return p;
 }
 
+template <class T, int DP, bool Two, int WM, int WN>
+static int run_strip(const AttnArgs& a, cudaStream_t s) {
+  static DeviceFlags ready;
+  using L = StripSmem<T, DP, WM, WN>;
+  if (set_smem_once(ready, attn_strip_kernel<T, DP, Two, WM, WN>, L::bytes) != FC_OK) return FC_ERR_CUDA;
+  attn_strip_kernel<T, DP, Two, WM, WN>
+      <<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, L::ROWS), a.KV, a.splits), L::threads, L::bytes, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
+}
 template <class T, int DP, bool Two>
 static int run_attn(bool few, const AttnArgs& a, cudaStream_t s) {
-  if (few) {
-    static DeviceFlags few_ready;
-    constexpr size_t bytes = FewSmem<T, DP>::bytes;
-    if (set_smem_once(few_ready, attn_few_kernel<T, DP, Two>, bytes) != FC_OK) return FC_ERR_CUDA;
-    attn_few_kernel<T, DP, Two><<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, 16), a.KV, a.splits), 128, bytes, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
-  }
-  static DeviceFlags ready;
-  constexpr size_t bytes = FwdSmem<T, DP>::bytes;
-  if (set_smem_once(ready, attn_fwd_kernel<T, DP, Two>, bytes) != FC_OK) return FC_ERR_CUDA;
-  attn_fwd_kernel<T, DP, Two><<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, 64), a.KV, a.splits), 128, bytes, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
+  if (few) return run_strip<T, DP, Two, 1, 4>(a, s);
+  // two halves of a key tile where a tile's bytes leave one block per SM: 128 molecules of 9 to 70
+  // atoms take 23 us with one and 30 with two, 2048 nodes of 8 FP32 heads of 128 the other way round
+  return run_strip<T, DP, Two, 4, (sizeof(T) == 4 && DP > 64) ? 2 : 1>(a, s);
 }
 
 template <class T>

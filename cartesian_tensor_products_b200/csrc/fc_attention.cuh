@@ -194,7 +194,6 @@ __device__ __forceinline__ void load_rows(T* tile, int D, int tid, Src src, Live
 template <class T, int DP, int ROWS, int THREADS, class Src1, class Src2, class Live>
 __device__ __forceinline__ void load_rows2(T* tile1, T* tile2, int D, int tid, Src1 src1, Src2 src2, Live live) {
   constexpr int VEC = 16 / sizeof(T), CH = DP / VEC, U = 8;
-  static_assert(ROWS * CH % THREADS == 0, "whole rounds");
 #pragma unroll 1
   for (int i0 = tid; i0 < ROWS * CH; i0 += U * THREADS) {
     bool ok[U];

@@ -39,17 +39,21 @@ __global__ void __launch_bounds__(256) attn_stat_kernel(AttnArgs a, const float*
   }
 }
 
+// Eight warps: 16 of the 64 resident rows and one half of every streamed tile
+// each; the halves' sums meet at the end.
 template <class T, int DP>
 struct VjpSmem {
   static constexpr int BN = kStep<T, DP> == 64 && DP > 64 ? 32 : kStep<T, DP>;   // streamed rows
   static constexpr int S = kStride<T, DP>;
-  static constexpr size_t bytes = sizeof(T) * 64 * S * 2 + sizeof(T) * BN * S * 4 + 4 * BN * sizeof(float4);
+  static constexpr size_t tiles = sizeof(T) * 64 * S * 2 + sizeof(T) * BN * S * 4;
+  static constexpr size_t bytes = tiles + 4 * BN * sizeof(float4);
+  static_assert(64 * (2 * DP + 3) * sizeof(float) <= tiles && bytes <= 232448, "shared memory");
 };
 
 // Query gradient, receiver position sums and slope sums.
 template <class T, int DP>
-__global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
-  constexpr int BN = VjpSmem<T, DP>::BN, NT = BN / 8, S = kStride<T, DP>;
+__global__ void __launch_bounds__(256) attn_vjp_q_kernel(AttnArgs a) {
+  constexpr int BN = VjpSmem<T, DP>::BN, BH = BN / 2, NT = BH / 8, S = kStride<T, DP>;
   extern __shared__ __align__(16) unsigned char smem[];
   T* qs = reinterpret_cast<T*>(smem);
   T* gs = qs + 64 * S;
@@ -58,7 +62,7 @@ __global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
   float4* info = reinterpret_cast<float4*>(vs + 2 * BN * S);
   TileAt at;
   if (!find_tile(a.recv_ptr, a.B, a.nr, a.G, 64, blockIdx.x, at)) return;
-  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) & 3, half = tid >> 7;
   int slo, shi;
   other_side(a.send_ptr, a.B, a.ns, at.b, slo, shi);
   const int all = shi > slo ? (shi - slo + BN - 1) / BN : 0;
@@ -70,12 +74,12 @@ __global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
     return base + vr / a.G * ld + (kvh * a.G + vr % a.G) * (long long)a.D;
   };
   auto inside = [&](int r) { return at.v0 + r < at.v1; };
-  load_rows<T, DP, 64, 128>(qs, a.D, tid, [&](int r) { return rowat(static_cast<const T*>(a.q), a.ldq, r); }, inside);
-  load_rows<T, DP, 64, 128>(gs, a.D, tid, [&](int r) { return rowat(static_cast<const T*>(a.g), a.ldg, r); }, inside);
+  load_rows<T, DP, 64, 256>(qs, a.D, tid, [&](int r) { return rowat(static_cast<const T*>(a.q), a.ldq, r); }, inside);
+  load_rows<T, DP, 64, 256>(gs, a.D, tid, [&](int r) { return rowat(static_cast<const T*>(a.g), a.ldg, r); }, inside);
   auto load_kv = [&](int t, int st) {
     const long long j0 = slo + (long long)t * BN;
     auto live = [&](int r) { return j0 + r < shi && (!a.mask || a.mask[j0 + r]); };
-    load_rows2<T, DP, BN, 128>(
+    load_rows2<T, DP, BN, 256>(
         ks + st * BN * S, vs + st * BN * S, a.D, tid, [&](int r) { return k + (j0 + r) * a.ldk; },
         [&](int r) { return v + (j0 + r) * a.ldv; }, live);
     if (tid < BN) {
@@ -127,12 +131,13 @@ __global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
       __syncthreads();
       continue;
     }
-    const float4* in = info + st * BN;
-    const long long left = shi - slo - (long long)t * BN;
-    const int nl = left >= BN ? NT : (int)(left + 7) / 8;   // column tiles that are there
+    const T *kt = ks + (st * BN + half * BH) * S, *vt = vs + (st * BN + half * BH) * S;
+    const float4* in = info + st * BN + half * BH;
+    const long long left = shi - slo - (long long)t * BN - half * BH;
+    const int nl = left >= BH ? NT : left <= 0 ? 0 : (int)(left + 7) / 8;   // column tiles that are there
     float s[NT][4], dp[NT][4];
-    strip_nt<T, DP, NT>(s, qs + warp * 16 * S, ks + st * BN * S, nl);
-    strip_nt<T, DP, NT>(dp, gs + warp * 16 * S, vs + st * BN * S, nl);
+    strip_nt<T, DP, NT>(s, qs + warp * 16 * S, kt, nl);
+    strip_nt<T, DP, NT>(dp, gs + warp * 16 * S, vt, nl);
     if (a.cap > 0.0f) strip_tanh<T, NT>(s, mul);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -164,10 +169,12 @@ __global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
         }
       }
     }
-    strip_pn<T, DP, NT, false>(acc, s, ks + st * BN * S, 1.0f, 1.0f, nl);
+    strip_pn<T, DP, NT, false>(acc, s, kt, 1.0f, 1.0f, nl);
     __syncthreads();
   }
   cp_wait<0>();
+  __syncthreads();
+  float* mg = reinterpret_cast<float*>(smem);   // [64] rows of the second half: DP values, four sums
 
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -178,7 +185,25 @@ __global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
       bz[h] += __shfl_xor_sync(0xffffffffu, bz[h], o);
       bs[h] += __shfl_xor_sync(0xffffffffu, bs[h], o);
     }
+    float* m = mg + (warp * 16 + g + 8 * h) * (DP + 4);
+    if (half == 1) {
+#pragma unroll
+      for (int d = 0; d < DP / 8; ++d) {
+        m[d * 8 + c2] = acc[d][2 * h];
+        m[d * 8 + c2 + 1] = acc[d][2 * h + 1];
+      }
+      if ((lane & 3) == 0) {
+        m[DP] = bx[h]; m[DP + 1] = by[h]; m[DP + 2] = bz[h]; m[DP + 3] = bs[h];
+      }
+    }
+  }
+  __syncthreads();
+  if (half == 1) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
     if (vr[h] >= at.v1) continue;
+    const float* m = mg + (warp * 16 + g + 8 * h) * (DP + 4);
+    bx[h] += m[DP]; by[h] += m[DP + 1]; bz[h] += m[DP + 2]; bs[h] += m[DP + 3];
     const long long row = vr[h] / a.G * a.H + kvh * a.G + (int)(vr[h] % a.G);
     const long long pr = (long long)blockIdx.z * a.nr * a.H + row;
     if (a.rowpart && (lane & 3) == 0)
@@ -187,7 +212,7 @@ __global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
 #pragma unroll
     for (int d = 0; d < DP / 8; ++d) {
       if (d * 8 >= a.D) continue;
-      const float v2[2] = {acc[d][2 * h] * a.scale, acc[d][2 * h + 1] * a.scale};
+      const float v2[2] = {(acc[d][2 * h] + m[d * 8 + c2]) * a.scale, (acc[d][2 * h + 1] + m[d * 8 + c2 + 1]) * a.scale};
       if (a.splits > 1)
         store_pack<float, 2>(a.part + pr * a.D + d * 8 + c2, v2);
       else
@@ -198,8 +223,8 @@ __global__ void __launch_bounds__(128) attn_vjp_q_kernel(AttnArgs a) {
 
 // Key and value gradients and sender position sums.
 template <class T, int DP>
-__global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
-  constexpr int BN = VjpSmem<T, DP>::BN, NT = BN / 8, S = kStride<T, DP>;
+__global__ void __launch_bounds__(256) attn_vjp_kv_kernel(AttnArgs a) {
+  constexpr int BN = VjpSmem<T, DP>::BN, BH = BN / 2, NT = BH / 8, S = kStride<T, DP>;
   extern __shared__ __align__(16) unsigned char smem[];
   T* ks = reinterpret_cast<T*>(smem);
   T* vs = ks + 64 * S;
@@ -209,7 +234,7 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
   float4* rst = rpos + 2 * BN;                                 // [2][BN]: log-sum, delta
   TileAt at;
   if (!find_tile(a.send_ptr, a.B, a.ns, 1, 64, blockIdx.x, at)) return;
-  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) & 3, half = tid >> 7;
   int rlo, rhi;
   other_side(a.recv_ptr, a.B, a.nr, at.b, rlo, rhi);
   const long long r0 = (long long)rlo * a.G, r1 = (long long)rhi * a.G;
@@ -217,9 +242,9 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
   const long long t0 = all * blockIdx.z / a.kv_splits, steps = all * (blockIdx.z + 1) / a.kv_splits - t0;
   auto shown = [&](long long j) { return j < at.v1 && (!a.mask || a.mask[j]); };
   auto live = [&](int r) { return shown(at.v0 + r); };
-  load_rows<T, DP, 64, 128>(
+  load_rows<T, DP, 64, 256>(
       ks, a.D, tid, [&](int r) { return static_cast<const T*>(a.k) + (at.v0 + r) * a.ldk + (long long)kvh * a.D; }, live);
-  load_rows<T, DP, 64, 128>(
+  load_rows<T, DP, 64, 256>(
       vs, a.D, tid, [&](int r) { return static_cast<const T*>(a.v) + (at.v0 + r) * a.ldv + (long long)kvh * a.D; }, live);
   auto load_q = [&](long long t, int st) {
     const long long b = r0 + (t0 + t) * BN;
@@ -227,9 +252,9 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
       return base + (b + r) / a.G * ld + (kvh * a.G + (b + r) % a.G) * (long long)a.D;
     };
     auto in = [&](int r) { return b + r < r1; };
-    load_rows<T, DP, BN, 128>(qs + st * BN * S, a.D, tid,
+    load_rows<T, DP, BN, 256>(qs + st * BN * S, a.D, tid,
                               [&](int r) { return at_row(static_cast<const T*>(a.q), a.ldq, r); }, in);
-    load_rows<T, DP, BN, 128>(gs + st * BN * S, a.D, tid,
+    load_rows<T, DP, BN, 256>(gs + st * BN * S, a.D, tid,
                               [&](int r) { return at_row(static_cast<const T*>(a.g), a.ldg, r); }, in);
     if (tid < BN) {
       float4 p = make_float4(0.f, 0.f, 0.f, 0.f), s = make_float4(INFINITY, 0.f, 0.f, 0.f);
@@ -281,12 +306,13 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
       __syncthreads();
       continue;
     }
-    const float4 *rp = rpos + st * BN, *rs = rst + st * BN;
-    const long long left = r1 - r0 - (t0 + t) * BN;
-    const int nl = left >= BN ? NT : (int)(left + 7) / 8;   // column tiles that are there
+    const T *qt = qs + (st * BN + half * BH) * S, *gt = gs + (st * BN + half * BH) * S;
+    const float4 *rp = rpos + st * BN + half * BH, *rs = rst + st * BN + half * BH;
+    const long long left = r1 - r0 - (t0 + t) * BN - half * BH;
+    const int nl = left >= BH ? NT : left <= 0 ? 0 : (int)(left + 7) / 8;   // column tiles that are there
     float s[NT][4], dp[NT][4];
-    strip_nt<T, DP, NT>(s, ks + warp * 16 * S, qs + st * BN * S, nl);
-    strip_nt<T, DP, NT>(dp, vs + warp * 16 * S, gs + st * BN * S, nl);
+    strip_nt<T, DP, NT>(s, ks + warp * 16 * S, qt, nl);
+    strip_nt<T, DP, NT>(dp, vs + warp * 16 * S, gt, nl);
     if (a.cap > 0.0f) strip_tanh<T, NT>(s, mul);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -318,11 +344,14 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
         }
       }
     }
-    strip_pn<T, DP, NT, false>(dv, s, gs + st * BN * S, 1.0f, 1.0f, nl);
-    strip_pn<T, DP, NT, false>(dk, dp, qs + st * BN * S, 1.0f, 1.0f, nl);
+    strip_pn<T, DP, NT, false>(dv, s, gt, 1.0f, 1.0f, nl);
+    strip_pn<T, DP, NT, false>(dk, dp, qt, 1.0f, 1.0f, nl);
     __syncthreads();
   }
   cp_wait<0>();
+  __syncthreads();
+  float* mg = reinterpret_cast<float*>(smem);   // [64] rows of the second half: DP and DP values, three sums
+  constexpr int MS = 2 * DP + 3;
 
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -332,7 +361,27 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
       by[h] += __shfl_xor_sync(0xffffffffu, by[h], o);
       bz[h] += __shfl_xor_sync(0xffffffffu, bz[h], o);
     }
+    float* m = mg + (warp * 16 + g + 8 * h) * MS;
+    if (half == 1) {
+#pragma unroll
+      for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m[d * 8 + c2 + e] = dk[d][2 * h + e];
+          m[DP + d * 8 + c2 + e] = dv[d][2 * h + e];
+        }
+      if ((lane & 3) == 0) {
+        m[2 * DP] = bx[h]; m[2 * DP + 1] = by[h]; m[2 * DP + 2] = bz[h];
+      }
+    }
+  }
+  __syncthreads();
+  if (half == 1) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
     if (vj[h] >= at.v1) continue;
+    const float* m = mg + (warp * 16 + g + 8 * h) * MS;
+    bx[h] += m[2 * DP]; by[h] += m[2 * DP + 1]; bz[h] += m[2 * DP + 2];
     if (a.colpart && (lane & 3) == 0)
       a.colpart[((long long)blockIdx.z * a.KV + kvh) * a.ns + vj[h]] =
           keep[h] ? make_float4(bx[h], by[h], bz[h], 0.f) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -341,8 +390,12 @@ __global__ void __launch_bounds__(128) attn_vjp_kv_kernel(AttnArgs a) {
 #pragma unroll
     for (int d = 0; d < DP / 8; ++d) {
       if (d * 8 >= a.D) continue;
-      const float k2[2] = {keep[h] ? dk[d][2 * h] * a.scale : 0.0f, keep[h] ? dk[d][2 * h + 1] * a.scale : 0.0f};
-      const float v2[2] = {keep[h] ? dv[d][2 * h] : 0.0f, keep[h] ? dv[d][2 * h + 1] : 0.0f};
+      float k2[2], v2[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        k2[e] = keep[h] ? (dk[d][2 * h + e] + m[d * 8 + c2 + e]) * a.scale : 0.0f;
+        v2[e] = keep[h] ? dv[d][2 * h + e] + m[DP + d * 8 + c2 + e] : 0.0f;
+      }
       if (a.kv_splits > 1) {
         const long long pr = ((long long)blockIdx.z * a.ns * a.KV + row) * a.D + d * 8 + c2;
         if (a.kb) store_pack<float, 2>(a.part_k + pr, k2);
@@ -454,10 +507,10 @@ static int run_strips(bool kv, const AttnArgs& a, cudaStream_t s) {
   if (kv) {
     if (set_smem_once(ready_kv, attn_vjp_kv_kernel<T, DP>, bytes) != FC_OK) return FC_ERR_CUDA;
     attn_vjp_kv_kernel<T, DP>
-        <<<dim3((unsigned)tile_slots(a.B, a.ns, 1, 64), a.KV, a.kv_splits), 128, bytes, s>>>(a);
+        <<<dim3((unsigned)tile_slots(a.B, a.ns, 1, 64), a.KV, a.kv_splits), 256, bytes, s>>>(a);
   } else {
     if (set_smem_once(ready_q, attn_vjp_q_kernel<T, DP>, bytes) != FC_OK) return FC_ERR_CUDA;
-    attn_vjp_q_kernel<T, DP><<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, 64), a.KV, a.splits), 128, bytes, s>>>(a);
+    attn_vjp_q_kernel<T, DP><<<dim3((unsigned)tile_slots(a.B, a.nr, a.G, 64), a.KV, a.splits), 256, bytes, s>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
 }
