@@ -291,16 +291,27 @@ static int parts(long long blocks, long long fill, long long per, int step) {
   return s < 1 ? 1 : (int)s;
 }
 
-#ifndef FC_TC_ROWS
-#define FC_TC_ROWS 96
-#endif
+// 16-bit rows go to the tcgen05 kernels from this many rows of an average
+// structure on (and 64 senders).  They hold 128 rows and pad the head to 64 or
+// 128 values, so wide heads gain first.  64 structures, 8 BF16 heads, capped and
+// biased, strips against tcgen05 in us:
+//   forward   D 128: 50 rows 37/39, 96 rows 66/49;  D 64: 96 rows 35/43, 192 rows 75/83,
+//             16 structures of 256 rows 35/29;  D 16: 256 rows 67/100, 16 of 512 72/69
+//   with gradient   D 128: 50 rows 172/145;  D 64: 64 rows 96/129, 80 rows 185/152;
+//             D 32: 256 rows 348/353
+static int tc_rows(int D, bool vjp) {
+  if (D > 64) return vjp ? 48 : 72;
+  if (D > 32) return vjp ? 72 : 128;
+  return 320;
+}
 AttnPlan attn_plan(const fc_attn_desc* d, int B, int nr, int ns) {
   AttnPlan p;
   const int G = d->heads / d->kv_heads, KV = d->kv_heads, sms = device_sm_count();
   const long long rows = (long long)nr * G, per_r = B > 0 ? rows / B : 0, per_s = B > 0 ? ns / B : 0;
   const int step = d->dtype == FC_F32 && d->head_dim > 64 ? 32 : 64;
-  p.tc = d->dtype != FC_F32 && per_r >= FC_TC_ROWS && per_s >= 128 && rows < (1ll << 31);
-  p.tc_vjp = p.tc && G <= 64;
+  const bool can = d->dtype != FC_F32 && per_s >= 64 && rows < (1ll << 31);
+  p.tc = can && per_r >= tc_rows(d->head_dim, false);
+  p.tc_vjp = can && per_r >= tc_rows(d->head_dim, true) && G <= 64;
   // few: up to two 16-row tiles a structure
   p.few = !p.tc && per_r <= 32;
   const auto tiles = [&](long long n, int tile) { return (n + tile - 1) / tile > B ? (n + tile - 1) / tile : B; };

@@ -13,6 +13,9 @@
  *   - fc_product_ladder     node-local correlation ladder, Sec. 5 Eq. (2)
  *                           with path-reduced products (App. E)
  *   - fc_product_ladder_vjp its vector-Jacobian product
+ * Operators on node rows that stand beside these (species embedding, head norm
+ * with position rotation, attention inside a structure) are declared in
+ * flashcart_nodes.h.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -419,7 +422,8 @@ int fc_full_ladder_vjp(const fc_ladder_desc *desc, int n_nodes, const float *A,
                        void *workspace, size_t ws_bytes, fc_stream_t stream);
 
 /* Sticky device-side error word of the kernels that wait on barriers (the
- * tensor-core mixes and maps of the ladders): each wait gives up after a
+ * tensor-core mixes and maps of the ladders, the tensor-core kernels of the
+ * node attention): each wait gives up after a
  * bounded time (fc_set_wait_timeout), skips the rest of its CTA's work --
  * after letting the copies and MMAs it already started finish -- and sets
  * the word instead of hanging; that call's outputs are then meaningless.

@@ -26,7 +26,8 @@
  * Memory.  Row arrays are 16-byte aligned, the others 4-byte aligned.
  * Outputs may not overlap inputs or each other.
  * Results.  No atomic additions of floating-point values: the same call gives
- * the same bits.
+ * the same bits.  The attention kernels that wait on barriers give up after a
+ * bounded time and set the word that fc_device_error reads.
  */
 #ifndef FLASHCART_NODES_H
 #define FLASHCART_NODES_H

@@ -282,6 +282,8 @@ ATTN = {
     "few senders": dict(recv=[1500, 900], send=[150, 140], h=4, kv=2, d=64, dtype=BF16, cap=9.0),
     "few senders f32": dict(recv=[1500, 900], send=[50, 70], h=4, kv=2, d=24, dtype=F32),
     "outside rows bf16": dict(recv=[200, 270], send=None, h=2, kv=2, d=64, dtype=BF16, lead=5, tail=350),
+    "narrow, many tiles": dict(recv=[700, 400], send=None, h=4, kv=2, d=24, dtype=F16, cap=6.0, hide=0.1),
+    "narrow apart": dict(recv=[400, 350], send=[90, 1500], h=3, kv=3, d=8, dtype=BF16),
     "many": dict(recv=[(7 * i) % 23 for i in range(300)], send=None, h=2, kv=2, d=16, dtype=F32),
 }
 
@@ -394,6 +396,70 @@ def test_wants_streams_and_workspaces(fc):
         fc.node_attention(q.transpose(0, 1), k, v, rp, **kw)
     with pytest.raises(TypeError):
         fc.node_attention(q, k.half(), v, rp, **kw)
+
+
+def test_waits_give_up_then_recover(fc):
+    """The tensor-core attention kernels' bounded waits at a bound of 1 ns: the calls return, the error word is set,
+    and with the default bound back the same calls give the same results."""
+    c = Case([700], None, 4, 4, 64, BF16, cap=8.0)
+    clean, cbars = c.run(fc)
+    assert fc.device_error() == 0
+    fc.set_wait_timeout(1)
+    try:
+        c.run(fc)
+        torch.cuda.synchronize()
+        flag = fc.device_error()
+    finally:
+        fc.set_wait_timeout(0)
+    assert flag == 1
+    assert fc.device_error() == 0          # the word was cleared by the read
+    got, bars = c.run(fc)
+    assert fc.device_error() == 0
+    for a, b in zip([*clean, *cbars], [*got, *bars]):
+        assert a is None or torch.equal(a, b)
+
+
+def test_calls_on_two_streams_at_once(fc):
+    """Two steps running beside each other, each with its own scratch."""
+    cases = [Case([500, 300], None, 4, 2, 64, BF16, cap=8.0, seed=s) for s in (1, 2)]
+    want = [c.run(fc) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(3):
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                got.append(c.run(fc))
+    torch.cuda.synchronize()
+    for i, (g, w) in enumerate(zip(got, want * 3)):
+        for a, b in zip([*g[0], *g[1]], [*w[0], *w[1]]):
+            assert a is None or torch.equal(a, b), i
+
+
+def test_rows_of_two_calls_in_one_capture_share_nothing(fc):
+    """Two captured graphs, replayed in turn, each with the scratch of its own pool."""
+    cases = [Case([260, 140], None, 4, 2, 32, F16, cap=8.0, seed=s) for s in (3, 4)]
+    want = [c.run(fc) for c in cases]
+    dev_in = []
+    for c in cases:
+        q, k, v = c.parts(dev(c.qw), dev(c.kw))
+        dev_in.append((q, k, v, dev(c.rp), dev(c.g), dict(c.kwargs(dev), send_ptr=dev(c.sp))))
+    graphs, outs = [], []
+    torch.cuda.synchronize()
+    for q, k, v, rp, g, kw in dev_in:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o = fc.node_attention(q, k, v, rp, residual=True, **kw)
+            outs.append((o, fc.node_attention_vjp(q, k, v, o[2], o[1], g, rp, **kw)))
+        graphs.append(graph)
+    for _ in range(2):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for (o, b), (wo, wb) in zip(outs, want):
+        for x, y in zip([*o, *b], [*wo, *wb]):
+            assert x is None or torch.equal(x, y)
 
 
 def test_capture_and_replay(fc):
