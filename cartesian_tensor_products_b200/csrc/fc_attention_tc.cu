@@ -37,7 +37,8 @@ struct RowScore {
   float2 mul, cap2, px, py, pz, sl;   // slope negated
   TanhPoly poly;
   __device__ __forceinline__ RowScore(const AttnArgs& a, long long node, int head)
-      : mul(pair(Cap ? a.scale / a.cap : a.scale * kLog2e)), cap2(pair(a.cap * kLog2e)), poly(a.cap * kLog2e) {
+      : mul(pair(Cap ? a.scale / a.cap : a.scale * kLog2e)), cap2(pair(a.cap * kLog2e)), poly(a.cap * kLog2e, mul.x) {
+    if (!Cap) poly.lim = INFINITY;
     px = py = pz = sl = pair(0.0f);
     if (Bias) {
       px = pair(a.pos_r[3 * node]);
@@ -68,7 +69,7 @@ struct RowScore {
 #pragma unroll
       for (int e = 0; e < 16; ++e) y[e] = add2(y[e], lds2(in + 3 * kAtStep + 2 * e));
   }
-  // 64 columns with the cap's polynomial; big: the largest score over the cap
+  // 64 columns with the cap's polynomial; big: the largest product
   template <bool Flags>
   __device__ __forceinline__ void easy(uint32_t st, const float* in, float neg_m, float2 (&x)[32], float& big) const {
     const float2 nm = pair(neg_m);
@@ -82,7 +83,7 @@ struct RowScore {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         if (Cap) {
-          const float2 v = mul2(pair_at(r[hf], e), mul);
+          const float2 v = pair_at(r[hf], e);
           b[e & 3] = max3_abs(b[e & 3], v.x, v.y);
           x[16 * hf + e] = fma2(v, poly(mul2(v, v)), nm);
         } else {
@@ -96,7 +97,7 @@ struct RowScore {
   // any scores; whether the polynomial would have served the warp
   __device__ __forceinline__ bool any(uint32_t st, const float* in, float neg_m, bool flags, float2 (&x)[32]) const {
     const float2 nm = pair(neg_m);
-    bool small = true;
+    float big = 0.0f;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t r[32];
@@ -106,7 +107,8 @@ struct RowScore {
 #pragma unroll
       for (int e = 0; e < 16; ++e) y[e] = Cap ? mul2(pair_at(r, e), mul) : fma2(pair_at(r, e), mul, nm);
       if (Cap) {
-        small &= tanh_in_range(y);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) big = max3_abs(big, y[e].x, y[e].y);
 #pragma unroll
         for (int e = 0; e < 16; ++e) y[e] = fma2(make_float2(cap_tanh<T>(y[e].x), cap_tanh<T>(y[e].y)), cap2, nm);
       }
@@ -117,7 +119,7 @@ struct RowScore {
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[16 * hf + e] = y[e];
     }
-    return small;
+    return !Cap || !__any_sync(0xffffffffu, !(big <= kAtTanhMax && poly.lim > 0.0f));
   }
 };
 
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
         const float mx = max_pairs(x);
         uint32_t w[PT][32];
         const float sum = weigh<T, PT>(x, w);
-        if (!__any_sync(0xffffffffu, !(big <= kTanhMax) || mx > (set ? 8.0f : -INFINITY))) {
+        if (!__any_sync(0xffffffffu, !(big <= score.poly.lim) || mx > (set ? 8.0f : -INFINITY))) {
 #pragma unroll
           for (int p = 0; p < PT; ++p) tc::tmem_st32(st + 32 * p, w[p]);
           l += sum;

@@ -95,17 +95,6 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
 __device__ __forceinline__ float2 pair_at(const uint32_t (&r)[32], int e) {
   return make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
 }
-// Whole warp: write 16 columns.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-      :
-      : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
 // Four rows of a panel: lane/8 of the rows, 16-byte chunk lane%8; dead rows and
 // chunks past the head become zeros.  dst: the panel's address at the first row.
 __device__ __forceinline__ void copy_rows4(uint32_t dst, int row, int lane, const void* src, bool live) {
@@ -133,7 +122,6 @@ __device__ __forceinline__ void load_panel(uint32_t dst, const CUtensorMap* map,
 // is one panel.  False if the driver refuses it.
 // (`group` heads of 64 / group rows, both counted down where they do not divide).
 bool at_tensor_map(CUtensorMap* m, bool half, const void* base, int D, int heads, long long ld, int rows, int group = 1);
-// error word and wait bound of these kernels (one of each per source file)
 
 // Descriptors (128-byte swizzle) of a tile whose panels have R rows, from byte
 // address a, and their 16-value or 16-row steps.
@@ -177,30 +165,31 @@ __device__ __forceinline__ float max_pairs(const float2 (&x)[N]) {
   return max3(fmaxf(m[0], m[1]), m[2], m[3]);
 }
 
-// tanh(x) / x for |x| <= 0.8, times f, for pairs (tanh_poly).
+// f tanh(mul s) / s for |mul s| <= 0.6, as a polynomial in s^2 with the powers of
+// mul in its coefficients (degree 4, least largest relative error, fitted to
+// tanh(x)/x: 7.3e-8).  The FP32 pipe is what the score arithmetic fills first, so
+// the narrower range of strip_tanh's 0.8 is given for two operations less.
+constexpr float kAtTanhMax = 0.6f;
 struct TanhPoly {
-  float2 c[6];
-  __device__ __forceinline__ explicit TanhPoly(float f) {
+  float2 c[5];
+  float lim;   // of |s|; a tiny mul, whose powers underflow, has no range
+  __device__ __forceinline__ TanhPoly(float f, float mul) {
+    const float k[5] = {0.9999999403953552f, -0.33332309126853943f, 0.13310173153877258f, -0.05210148170590401f,
+                        0.015475427731871605f};
+    const float m2 = mul * mul;
+    float p = f * mul;
 #pragma unroll
-    for (int i = 0; i < 6; ++i) c[i] = pair(f * tanh_c(i));
+    for (int i = 0; i < 5; ++i) {
+      c[i] = pair(p * k[i]);
+      p *= m2;
+    }
+    lim = fabsf(mul) >= 1e-4f ? kAtTanhMax / fabsf(mul) : -1.0f;
   }
   __device__ __forceinline__ float2 operator()(float2 z) const {
-    float2 p = fma2(z, c[5], c[4]);
-    p = fma2(z, p, c[3]);
+    float2 p = fma2(z, c[4], c[3]);
     p = fma2(z, p, c[2]);
     p = fma2(z, p, c[1]);
     return fma2(z, p, c[0]);
   }
 };
-// Whether a warp's scores over the cap stay in the polynomial's range.  They
-// nearly always do; the special-function unit is then left to exp and the
-// distances.  A warp that holds a larger one (or NaN) takes cap_tanh.
-template <int N>
-__device__ __forceinline__ bool tanh_in_range(const float2 (&x)[N]) {
-  float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < N; ++i) m[i & 3] = max3_abs(m[i & 3], x[i].x, x[i].y);
-  return !__any_sync(0xffffffffu, !(max3(fmaxf(m[0], m[1]), m[2], m[3]) <= kTanhMax));
-}
-
 }  // namespace fc

@@ -44,14 +44,14 @@ struct AtVjp {
 template <class T, bool Cap, bool Bias, bool KV>
 struct RowGrad {
   float2 mul, cap2, px, py, pz, sl, nl, nd;   // negated: slope (base 2), log-sum, delta
-  float cap_f;
+  TanhPoly poly;
+  __device__ __forceinline__ explicit RowGrad(float m) : mul(pair(m)), poly(1.0f, m) {}
   // P (KV) and dS of 64 columns as 16-bit pairs; sums: position x, y, z, slope (query gradient)
   // (and, for the query gradient: the weights' sums of the same four, and the sum of dt)
   static constexpr int kSums = KV ? 3 : 9;
   template <bool Easy, bool Flags>
   __device__ __forceinline__ void tile(uint32_t st, const float* in, uint32_t (&w)[KV ? 2 : 1][32],
                                        float2 (&sum)[kSums], float& big) const {
-    const TanhPoly poly(1.0f);
     float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kSums; ++i) sum[i] = pair(0.0f);
@@ -68,13 +68,14 @@ struct RowGrad {
         const float2 cl = KV ? lds2(f + 3 * kAtStep + 2 * e) : nl;
         float2 t, dc;
         if (Cap) {
-          const float2 v = mul2(pair_at(rs, e), mul);
+          const float2 v = pair_at(rs, e);
           float2 th;
           if (Easy) {
             b[e & 3] = max3_abs(b[e & 3], v.x, v.y);
             th = mul2(v, poly(mul2(v, v)));
           } else {
-            th = make_float2(cap_tanh<T>(v.x), cap_tanh<T>(v.y));
+            const float2 x = mul2(v, mul);
+            th = make_float2(cap_tanh<T>(x.x), cap_tanh<T>(x.y));
           }
           t = fma2(th, cap2, cl);
           dc = fma2(make_float2(-th.x, -th.y), th, pair(1.0f));
@@ -324,8 +325,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_vjp_tc_kernel(AttnArgs a, 
     const uint32_t u = (uint32_t)(keep ? vr : at.v0);
     const long long node = KV ? u : u / (uint32_t)a.G;
     const int head = KV ? kvh : kvh * a.G + (int)(u - (uint32_t)node * a.G);
-    RowGrad<T, Cap, Bias, KV> grad;
-    grad.mul = pair(Cap ? a.scale / a.cap : a.scale * kLog2e);
+    RowGrad<T, Cap, Bias, KV> grad(Cap ? a.scale / a.cap : a.scale * kLog2e);
     grad.cap2 = pair(a.cap * kLog2e);
     grad.px = grad.py = grad.pz = grad.sl = grad.nd = pair(0.0f);
     grad.nl = pair(-INFINITY);
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_vjp_tc_kernel(AttnArgs a, 
           grad.template tile<true, true>(st, in, w, add, big);
         else
           grad.template tile<true, false>(st, in, w, add, big);
-        ok = !Cap || !__any_sync(0xffffffffu, !(big <= kTanhMax));
+        ok = !Cap || !__any_sync(0xffffffffu, !(big <= grad.poly.lim));
         easy = ok;
       } else {
         easy = (i & 14) == 0;   // try the polynomial again now and then
