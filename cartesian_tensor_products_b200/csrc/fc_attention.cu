@@ -275,7 +275,8 @@ int check_attn(const fc_attn_desc* d, int n_struct, int n_recv, int n_send) {
   if (d->heads < 1 || d->kv_heads < 1 || d->heads > 1024 || d->kv_heads > d->heads || d->heads % d->kv_heads)
     return FC_ERR_ARG;
   if (d->head_dim < 8 || d->head_dim > 128) return FC_ERR_ARG;
-  if (!isfinite(d->scale) || !isfinite(d->cap) || d->cap < 0.0f) return FC_ERR_ARG;
+  if (!isfinite(d->scale * kLog2e) || !isfinite(d->cap * kLog2e) || d->cap < 0.0f) return FC_ERR_ARG;
+  if (d->cap > 0.0f && !isfinite(d->scale / d->cap)) return FC_ERR_ARG;   // 0 times it would be NaN
   if (d->head_dim % 8) return FC_ERR_ALIGN;
   return FC_OK;
 }

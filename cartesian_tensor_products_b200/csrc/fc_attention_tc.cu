@@ -235,8 +235,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
       __syncwarp();
     } else {
       // ---------------- copies ----------------
-      // Warp cw copies tiles cw, cw + 3, ..: each waits for its own copies only.
-      // All three copy the receivers' rows first.
       // Warp cw brings in tiles cw, cw + 3, ..; all three copy the receivers' rows first.
       const int cw = warp - 9;
       const T* q = static_cast<const T*>(a.q);

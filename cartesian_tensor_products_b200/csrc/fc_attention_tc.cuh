@@ -119,8 +119,8 @@ __device__ __forceinline__ void load_panel(uint32_t dst, const CUtensorMap* map,
       : "memory");
 }
 // [rows][heads][D] of 16-bit values, row step ld, as {D, heads, rows}; the box
-// is one panel.  False if the driver refuses it.
-// (`group` heads of 64 / group rows, both counted down where they do not divide).
+// is one panel: `group` heads of 64 / group rows (rounded down).  False if the
+// driver refuses it.
 bool at_tensor_map(CUtensorMap* m, bool half, const void* base, int D, int heads, long long ld, int rows, int group = 1);
 
 // Descriptors (128-byte swizzle) of a tile whose panels have R rows, from byte
@@ -172,7 +172,7 @@ __device__ __forceinline__ float max_pairs(const float2 (&x)[N]) {
 constexpr float kAtTanhMax = 0.6f;
 struct TanhPoly {
   float2 c[5];
-  float lim;   // of |s|; a tiny mul, whose powers underflow, has no range
+  float lim;   // of |s|; where a coefficient under- or overflows there is no range
   __device__ __forceinline__ TanhPoly(float f, float mul) {
     const float k[5] = {0.9999999403953552f, -0.33332309126853943f, 0.13310173153877258f, -0.05210148170590401f,
                         0.015475427731871605f};
@@ -183,7 +183,8 @@ struct TanhPoly {
       c[i] = pair(p * k[i]);
       p *= m2;
     }
-    lim = fabsf(mul) >= 1e-4f ? kAtTanhMax / fabsf(mul) : -1.0f;
+    const float lo = fminf(fabsf(c[0].x), fabsf(c[4].x)), hi = fmaxf(fabsf(c[0].x), fabsf(c[4].x));
+    lim = lo > 1e-37f && hi < 1e37f ? kAtTanhMax / fabsf(mul) : -1.0f;
   }
   __device__ __forceinline__ float2 operator()(float2 z) const {
     float2 p = fma2(z, c[4], c[3]);

@@ -111,8 +111,8 @@ typedef struct {
   int heads;
   int kv_heads;
   int head_dim;
-  float scale; /* finite */
-  float cap;   /* 0: scores as they are; > 0: cap tanh(score / cap) */
+  float scale; /* |scale| < 2e38 */
+  float cap;   /* 0: scores as they are; > 0 (and < 2e38, scale / cap finite): cap tanh(score / cap) */
 } fc_attn_desc;
 
 /* Attention of the nodes of a batch of structures, receivers i to senders j
@@ -133,7 +133,8 @@ typedef struct {
  *   q [n_recv] rows of heads, k and v [n_send] rows of kv_heads; steps ldq,
  *   ldk, ldv.  pos_recv [n_recv][3], pos_send [n_send][3], slope [heads]:
  *   the distance bias, all NULL for none; pos_send NULL: the senders are the
- *   receivers (n_send = n_recv) and pos_recv serves both.
+ *   receivers (n_send = n_recv) and pos_recv serves both.  Positions are
+ *   finite, with distances below 1e18 (their squares are formed in FP32).
  *   send_mask [n_send] bytes, 0 hides a sender (its key and value rows are
  *   not used, whatever they hold); NULL hides none.
  *   out [n_recv] rows of heads, step ldo; lse [n_recv][heads] FP32 (natural
@@ -165,7 +166,10 @@ int fc_node_attention(const fc_attn_desc *desc, int n_struct, int n_recv, int n_
  *   of out (step ldg); lse itself takes no gradient.
  *   q_bar, k_bar, v_bar packed ([n][heads][head_dim], rows' type), slope_bar
  *   [heads], pos_*_bar [n][3]: each may be NULL to skip it.  Hidden senders
- *   get 0.
+ *   get 0.  16-bit types round P and ds / scale to the rows' type ahead of the
+ *   products; FP16 then has 6e-8 as its smallest step and 65504 as its largest
+ *   value, so that g should be scaled (as FP16 losses are) to keep P (g.v)
+ *   between them.  Slopes and positions do not pass through 16 bits.
  * workspace: fc_node_attention_vjp_workspace_size() bytes, 16-byte aligned. */
 size_t fc_node_attention_vjp_workspace_size(const fc_attn_desc *desc, int n_struct, int n_recv, int n_send);
 int fc_node_attention_vjp(const fc_attn_desc *desc, int n_struct, int n_recv, int n_send,

@@ -117,6 +117,12 @@ def test_attention_refusals(fc, vjp):
         assert attn(fc, True, qb=ODD) == ALIGN and attn(fc, True, prb=OFF) == ALIGN and attn(fc, True, o32=ODD) == ALIGN
 
 
+@pytest.mark.parametrize("vjp", [False, True])
+def test_attention_refuses_factors_that_overflow(fc, vjp):
+    for bad in (dict(cap=1e-38, scale=1e3), dict(cap=3e38), dict(scale=3e38), dict(scale=-3e38)):
+        assert attn(fc, vjp, **bad) == ARG, bad
+
+
 def test_python_entries_refuse_cpu_tensors(fc):
     x = torch.zeros(4, 3, 8)
     i = torch.zeros(4, dtype=torch.int32)

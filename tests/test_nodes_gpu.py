@@ -321,6 +321,37 @@ def test_nan_stays_in_its_structure_and_behind_the_mask(fc):
             assert torch.equal(a[40:], b[40:])
 
 
+@pytest.mark.parametrize("d,group", [(64, 1), (128, 2)])
+def test_nan_stays_in_its_structure_on_the_tensor_cores(fc, d, group):
+    """The same at lengths that the tcgen05 kernels take; structures end inside their tiles of 64 and 128 rows."""
+    c = Case([150, 130, 210], None, 4, 4 // group, d, BF16, cap=3.0, hide=0.2)
+    c.mask[170] = 0
+    clean, cbars = c.run(fc)
+    hidden = int((c.mask[280:490] == 0).nonzero()[0]) + 280
+    c.kw[hidden] = float("nan")
+    c.kw[170] = float("inf")
+    got, bars = c.run(fc)
+    for a, b in zip([*clean, *cbars], [*got, *bars]):
+        assert a is None or torch.equal(a, b)
+    c.qw[:150], c.kw[:150], c.pos[:150] = (float("nan"),) * 3
+    got, bars = c.run(fc)
+    for a, b in zip([*clean, *cbars[:4]], [*got, *bars[:4]]):
+        assert torch.equal(a[150:], b[150:])
+    assert fc.device_error() == 0
+
+
+@pytest.mark.parametrize("power", [-10, 10])
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_score_factors_far_from_one(fc, power, d):
+    """Queries and keys times 2^power and scale times 4^-power (exact in BF16) are the same scores, however large or
+    small scale / cap is then; the bounds scale along."""
+    c = Case([310], None, 2, 2, d, BF16, cap=3.0)
+    c.qw *= 2.0 ** power
+    c.kw[:, : c.kv] *= 2.0 ** power
+    c.scale *= 4.0 ** -power
+    c.check(fc)
+
+
 def test_coincident_nodes(fc):
     """Distance 0 between different nodes: no gradient, and no NaN."""
     c = Case([30], None, 2, 2, 16, F32)
