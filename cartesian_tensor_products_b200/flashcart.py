@@ -568,6 +568,13 @@ def _on(t, dtype, name, index, shape):
     return t.data_ptr()
 
 
+def _counts(*sizes):
+    """Sizes as the library takes them: ctypes would drop the bits from 32 on."""
+    for n in sizes:
+        if not 0 <= n < 1 << 31:
+            raise ValueError("size %d is outside 0 .. 2^31 - 1" % n)
+
+
 def _row_dtype(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
@@ -631,6 +638,7 @@ def species_embed(species, table, lmax=0, scale=1.0, out=None, stream=None):
     if species.dim() != 1 or table.dim() != 2:
         raise ValueError("species [N] and table [n_species][C] expected")
     (N,), (V, C) = species.shape, table.shape
+    _counts(N, V, C, lmax)
     shape = (N, (lmax + 1) ** 2 * C)
     if out is None:
         out = table.new_empty(shape)
@@ -645,10 +653,12 @@ def species_embed_vjp(species, g, n_species, lmax=0, scale=1.0, workspace=None, 
     """table_bar [n_species][C] (float32) of species_embed for the gradient g
     [N][(lmax+1)^2 C] of its output: the rank-0 rows summed by species."""
     index, dtype = species.get_device(), _row_dtype(g, "g")
+    _counts(n_species, lmax)
     NY = (lmax + 1) ** 2
     if species.dim() != 1 or g.dim() != 2 or g.shape[1] % NY:
         raise ValueError("species [N] and g [N][(lmax+1)^2 C] expected")
     N, C = species.shape[0], g.shape[1] // NY
+    _counts(N, C)
     bar = torch.empty((n_species, C), dtype=_F32, device=index)
     need = _scratch_size(index, "fc_species_embed_vjp_workspace_size", None, N, n_species, C)
     workspace, ws, size = _bytes(workspace, need, index)
@@ -667,6 +677,7 @@ def _head_desc(*fields):
 def _head_args(x, heads_q, gamma_q, gamma_k, pos, freq, eps):
     index, dtype = x.get_device(), _row_dtype(x, "x")
     N, H, D = _rows3(x, "x")
+    _counts(N, H, D)
     px, ldx = _rows(x, "x", x.dtype, index, (N, H, D))
     if not 0 <= heads_q <= H:
         raise ValueError("heads_q %d of %d heads" % (heads_q, H))
@@ -726,6 +737,7 @@ def _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask, sca
     index, dtype = q.get_device(), _row_dtype(q, "q")
     nr, H, D = _rows3(q, "q")
     ns, KV, _ = _rows3(k, "k")
+    _counts(nr, ns, H, KV, D)
     if recv_ptr.dim() != 1 or recv_ptr.shape[0] < 1:
         raise ValueError("recv_ptr shape %s" % (tuple(recv_ptr.shape),))
     if send_ptr is None:
@@ -737,6 +749,7 @@ def _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask, sca
     if pos is not None and pos_send is None and nr != ns:
         raise ValueError("pos_send is needed where senders are not the receivers")
     B1 = recv_ptr.shape[0]
+    _counts(B1)
     args = (_on(recv_ptr, _I32, "recv_ptr", index, (B1,)), _on(send_ptr, _I32, "send_ptr", index, (B1,)),
             *_rows(q, "q", q.dtype, index, (nr, H, D)), *_rows(k, "k", q.dtype, index, (ns, KV, D)),
             *_rows(v, "v", q.dtype, index, (ns, KV, D)), _on(pos, _F32, "pos", index, (nr, 3)),

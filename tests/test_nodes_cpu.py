@@ -123,6 +123,13 @@ def test_attention_refuses_factors_that_overflow(fc, vjp):
         assert attn(fc, vjp, **bad) == ARG, bad
 
 
+def test_python_sizes_fit_the_library(fc):
+    fc._counts(0, 2 ** 31 - 1)
+    for bad in (2 ** 31, 2 ** 32 + 5, -1):
+        with pytest.raises(ValueError):
+            fc._counts(1, bad)
+
+
 def test_python_entries_refuse_cpu_tensors(fc):
     x = torch.zeros(4, 3, 8)
     i = torch.zeros(4, dtype=torch.int32)

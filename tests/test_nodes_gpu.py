@@ -352,6 +352,25 @@ def test_score_factors_far_from_one(fc, power, d):
     c.check(fc)
 
 
+def test_sizes_past_32_bits_are_refused(fc):
+    """Counts that a 32-bit int cannot hold, from expanded tensors of one element: refused before any launch."""
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rows = torch.zeros(1, 1, 8, device="cuda")
+    for n in (2 ** 31, 2 ** 32 + 5):
+        with pytest.raises(ValueError):
+            fc.species_embed(one.expand(n), torch.zeros(2, 8, device="cuda"))
+        with pytest.raises(ValueError):
+            fc.species_embed_vjp(one, torch.zeros(1, 8, device="cuda"), n)
+        with pytest.raises(ValueError):
+            fc.head_norm_rotate(rows.expand(n, 1, 8), 1)
+        with pytest.raises(ValueError):
+            fc.node_attention(rows, rows.expand(n, 1, 8), rows.expand(n, 1, 8), one, one)
+        with pytest.raises(ValueError):
+            fc.node_attention(rows, rows, rows, one.expand(n))
+    with pytest.raises(ValueError):
+        fc.species_embed_vjp(one, torch.zeros(1, 8, device="cuda"), 3, lmax=-1)
+
+
 def test_coincident_nodes(fc):
     """Distance 0 between different nodes: no gradient, and no NaN."""
     c = Case([30], None, 2, 2, 16, F32)
