@@ -47,12 +47,18 @@ struct VjpSmem {
   static constexpr int S = kStride<T, DP>;
   static constexpr size_t tiles = sizeof(T) * 64 * S * 2 + sizeof(T) * BN * S * 4;
   static constexpr size_t bytes = tiles + 4 * BN * sizeof(float4);
+  // Blocks per SM that the registers are held to.  A short structure is one tile
+  // per block, whose latency a second block hides: 128 molecules of 9 to 70
+  // atoms, 8 heads, gradient in us with one / two: FP32 32-wide 156/115, BF16
+  // 64-wide 128/103 (spills and all).  FP32 64-wide is the other way round on
+  // long structures (4 of 300 to 900 nodes 601/651; the molecules 233/201).
+  static constexpr int blocks = sizeof(T) == 2 || DP <= 32 ? 2 : 1;
   static_assert(64 * (2 * DP + 3) * sizeof(float) <= tiles && bytes <= 232448, "shared memory");
 };
 
 // Query gradient, receiver position sums and slope sums.
 template <class T, int DP>
-__global__ void __launch_bounds__(256) attn_vjp_q_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(256, VjpSmem<T, DP>::blocks) attn_vjp_q_kernel(AttnArgs a) {
   constexpr int BN = VjpSmem<T, DP>::BN, BH = BN / 2, NT = BH / 8, S = kStride<T, DP>;
   extern __shared__ __align__(16) unsigned char smem[];
   T* qs = reinterpret_cast<T*>(smem);
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(256) attn_vjp_q_kernel(AttnArgs a) {
 
 // Key and value gradients and sender position sums.
 template <class T, int DP>
-__global__ void __launch_bounds__(256) attn_vjp_kv_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(256, VjpSmem<T, DP>::blocks) attn_vjp_kv_kernel(AttnArgs a) {
   constexpr int BN = VjpSmem<T, DP>::BN, BH = BN / 2, NT = BH / 8, S = kStride<T, DP>;
   extern __shared__ __align__(16) unsigned char smem[];
   T* ks = reinterpret_cast<T*>(smem);
