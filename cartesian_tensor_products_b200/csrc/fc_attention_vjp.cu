@@ -430,20 +430,44 @@ __global__ void __launch_bounds__(256) attn_vjp_join_kernel(long long rows, int 
   store_pack<T, 4>(to + row * D + c, acc);
 }
 
-// Position gradients, one warp per node: a receiver's parts and heads, a
-// sender's key heads, or both where the senders are the receivers.
-__global__ void __launch_bounds__(256) attn_pos_kernel(AttnArgs a, bool recv, bool send, int n, float* __restrict__ bar) {
-  const int lane = threadIdx.x & 31;
-  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= n) return;
+// The sums over heads and nodes, in one launch (the parts are small: 128
+// molecules took 4 us for the positions and 6 for the slopes one after the
+// other).  Blocks 0 .. slopes - 1: the slope gradient of one head, summed in
+// FP64, as the terms of a row cancel and there is one for every row.  Then the
+// position gradients, one warp per node: `recv` blocks for the receivers' parts
+// and heads (with the sender's key heads where the senders are the receivers),
+// the rest for the senders' key heads.
+__global__ void __launch_bounds__(256) attn_sums_kernel(AttnArgs a, int slopes, int recv, bool self,
+                                                        float* __restrict__ pos_recv, float* __restrict__ pos_send,
+                                                        float* __restrict__ slope) {
+  __shared__ double sum[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = (int)blockIdx.x - slopes;
+  if (block < 0) {
+    const int h = blockIdx.x;
+    double v = 0.0;
+    for (int s = 0; s < a.splits; ++s)
+#pragma unroll 8
+      for (long long i = threadIdx.x; i < a.nr; i += 256) v += a.rowpart[((long long)s * a.nr + i) * a.H + h].w;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) sum[warp] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < 8; ++w) v += sum[w];
+      slope[h] = (float)v;
+    }
+    return;
+  }
+  const bool of_recv = block < recv, of_send = !of_recv || self;
+  const long long i = (long long)(of_recv ? block : block - recv) * 8 + warp;
+  if (i >= (of_recv ? a.nr : a.ns)) return;
   float x = 0.f, y = 0.f, z = 0.f;
-  if (recv)
+  if (of_recv)
     for (int e = lane; e < a.splits * a.H; e += 32) {
       const int sp = e / a.H;
       const float4 v = a.rowpart[((long long)sp * a.nr + i) * a.H + (e - sp * a.H)];
       x += v.x; y += v.y; z += v.z;
     }
-  if (send)
+  if (of_send)
     for (int e = lane; e < a.KV * a.kv_splits; e += 32) {
       const float4 v = a.colpart[(long long)e * a.ns + i];
       x += v.x; y += v.y; z += v.z;
@@ -454,25 +478,8 @@ __global__ void __launch_bounds__(256) attn_pos_kernel(AttnArgs a, bool recv, bo
     z += __shfl_xor_sync(0xffffffffu, z, o);
   }
   if (lane == 0) {
-    bar[3 * i] = x; bar[3 * i + 1] = y; bar[3 * i + 2] = z;
-  }
-}
-
-// Slope gradient of one head per block, summed in FP64: the terms of a row
-// cancel, and there is one for every row.
-__global__ void __launch_bounds__(256) attn_slope_kernel(AttnArgs a, float* __restrict__ bar) {
-  __shared__ double sum[8];
-  const int h = blockIdx.x;
-  double v = 0.0;
-  for (int s = 0; s < a.splits; ++s)
-#pragma unroll 4
-    for (long long i = threadIdx.x; i < a.nr; i += 256) v += a.rowpart[((long long)s * a.nr + i) * a.H + h].w;
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = v;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 8; ++w) v += sum[w];
-    bar[h] = (float)v;
+    float* bar = (of_recv ? pos_recv : pos_send) + 3 * i;
+    bar[0] = x; bar[1] = y; bar[2] = z;
   }
 }
 
@@ -559,11 +566,11 @@ static int run_vjp(int dtype, const AttnArgs& a, const VjpWants& w, bool tc, con
     }
   }
   if (rc != FC_OK) return rc;
-  if (w.pos_recv_bar && a.nr > 0)
-    attn_pos_kernel<<<blocks(a.nr, 8), 256, 0, s>>>(sums, true, w.self, a.nr, w.pos_recv_bar);
-  if (w.pos_send_bar && a.ns > 0)
-    attn_pos_kernel<<<blocks(a.ns, 8), 256, 0, s>>>(sums, false, true, a.ns, w.pos_send_bar);
-  if (w.slope_bar) attn_slope_kernel<<<a.H, 256, 0, s>>>(sums, w.slope_bar);
+  const int slopes = w.slope_bar ? a.H : 0;
+  const unsigned recv = w.pos_recv_bar ? blocks(a.nr, 8) : 0, send = w.pos_send_bar ? blocks(a.ns, 8) : 0;
+  if (slopes + recv + send > 0)
+    attn_sums_kernel<<<slopes + recv + send, 256, 0, s>>>(sums, slopes, (int)recv, w.self, w.pos_recv_bar, w.pos_send_bar,
+                                                          w.slope_bar);
   return cudaGetLastError() == cudaSuccess ? FC_OK : FC_ERR_CUDA;
 }
 
