@@ -16,6 +16,11 @@
 // groups take the tiles in turn, so that one's arithmetic runs beside the
 // other's products.  The heads of a key head are rows of the stream tile
 // (64 / G receivers by G heads), so their sum needs no atomics.
+//
+// Bound like the forward, with the FP32 pipe ahead of the special functions (60 and
+// 32 % busy in the query gradient, 50 and 33 % in the other).  Forward and
+// gradient of 4096 nodes, 8 BF16 heads of 64, cap and bias: 653 us, the two
+// kernels here 246 and 241 us of it.
 #include <math.h>
 
 #include "fc_attention_tc.cuh"

@@ -11,6 +11,10 @@
 // exchange.  W is the widest vector that R is a multiple of (any R is valid:
 // odd ones take scalar units).  Angles are formed in FP64 and reduced to half
 // turns, since FP32 would lose the phase of positions far from the origin.
+// 65,536 nodes of 16 + 4 BF16 heads of 64: 336 MB in 75 us (4.5 TB/s; some 17
+// instructions a value, angles included, at a third of the warps); the VJP at
+// 32,769 nodes of 8 + 2 BF16 heads of 128: 252 MB in 100 us (its registers leave
+// two blocks per SM).
 #include <math.h>
 
 #include "fc_device.cuh"
