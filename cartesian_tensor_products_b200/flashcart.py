@@ -552,7 +552,9 @@ def _node_op(f):
 
 
 def _on(t, dtype, name, index, shape):
-    """Address of a contiguous tensor on device `index`; None passes as NULL."""
+    """Address of a contiguous tensor on device `index`; None passes as NULL.  A
+    tensor without elements has address 0, which would read as None: it passes
+    as an aligned address that nothing follows."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -565,7 +567,7 @@ def _on(t, dtype, name, index, shape):
         raise ValueError("%s shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    return t.data_ptr() or 16
 
 
 def _counts(*sizes):

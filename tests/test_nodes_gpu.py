@@ -371,6 +371,72 @@ def test_sizes_past_32_bits_are_refused(fc):
         fc.species_embed_vjp(one, torch.zeros(1, 8, device="cuda"), 3, lmax=-1)
 
 
+@pytest.mark.parametrize("dtype,d", [(F32, 32), (BF16, 64)])
+def test_one_side_without_rows(fc, dtype, d):
+    """No senders at all: zero rows, log-sum -infinity, zero gradients.  No receivers at all: the senders' gradients 0."""
+    q, g = (torch.randn(150, 4, d, device="cuda").to(dtype) for _ in range(2))
+    k = torch.empty(0, 2, d, dtype=dtype, device="cuda")
+    pos, none, slope = torch.rand(150, 3, device="cuda"), torch.empty(0, 3, device="cuda"), torch.ones(4, device="cuda")
+    ptr, zero = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 20, 150], [0, 0, 0]))
+    out, lse, o32 = fc.node_attention(q, k, k, ptr, zero, pos, none, slope, residual=True)
+    assert not out.any() and bool((lse == -math.inf).all())
+    bars = fc.node_attention_vjp(q, k, k, o32, lse, g, ptr, zero, pos, none, slope)
+    assert not any(bool(b.any()) for b in bars)
+    k, q0 = q[:, :2], q[:0]
+    out, lse, o32 = fc.node_attention(q0, k, k, zero, ptr, none, pos, slope, residual=True)
+    assert out.shape == (0, 4, d) and lse.shape == (0, 4)
+    bars = fc.node_attention_vjp(q0, k, k, o32, lse, q0, zero, ptr, none, pos, slope)
+    assert not any(bool(b.any()) for b in bars)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+def test_many_structures_of_one_node(fc, dtype):
+    """70,000 structures of one node: its weight is 1, so that the output is the value row and the log-sum the score."""
+    n = 70000
+    f = torch.randn(n, 3, 16, device="cuda").to(dtype)
+    q, k, v = f[:, :1], f[:, 1:2], f[:, 2:]
+    ptr = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    out, lse, o32 = fc.node_attention(q, k, v, ptr, residual=True)
+    # FP32 values go in as two TF32 ones of 11 bits: a part of 2^-10 is left by the first, of that again by the second
+    close(out, v.double().cpu(), (2.0 ** -20 if dtype == F32 else 0.0) * v.double().abs().cpu())
+    ref = (q.double() * k.double()).sum(-1).cpu() / 4
+    close(lse, ref, FWD_TOL * float(ref.abs().max()))
+    qb, kb, vb = fc.node_attention_vjp(q, k, v, o32, lse, v, ptr)[:3]
+    # P = exp2(t - log-sum) is 1 up to the rounding of both; in FP16 it is then rounded to 1 or a neighbour
+    close(vb, v.double().cpu(), (2 * R.u(dtype) + VJP_TOL) * v.double().abs().cpu() + sub(dtype))
+
+
+def test_offsets_past_32_bits(fc):
+    """Rows 65,536 values apart, 4.6e9 in all: the same results as from packed copies."""
+    n, ld = 70000, 65536
+    wide = torch.empty(n, ld, dtype=BF16, device="cuda")
+    col = ld - 3 * 2 * 64
+    wide[:, col:] = torch.randn(n, 3 * 2 * 64, device="cuda").to(BF16)
+    f = wide[:, col:].unflatten(1, (6, 64))
+    q, k, v = f[:, :2], f[:, 2:4], f[:, 4:]
+    packed = [t.contiguous() for t in (q, k, v)]
+    pos, freq = torch.rand(n, 3, device="cuda") * 9, torch.rand(3, 32, device="cuda")
+    assert torch.equal(fc.head_norm_rotate(f[:, :4], 2, pos=pos, freq=freq),
+                       fc.head_norm_rotate(f[:, :4].contiguous(), 2, pos=pos, freq=freq))
+    for lens in (350, 20):    # structures for the tensor cores, and short ones
+        ptr = torch.arange(0, n + 1, lens, dtype=torch.int32, device="cuda")
+        kw = dict(pos=pos, slope=torch.ones(2, device="cuda"))
+        a, b = (fc.node_attention(*t, ptr, residual=True, **kw) for t in ((q, k, v), packed))
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        a, b = (fc.node_attention_vjp(*t, a[2], a[1], g, ptr, **kw) for t, g in (((q, k, v), v), (packed, packed[2])))
+        assert all(torch.equal(x, y) for x, y in zip(a, b) if x is not None)
+    del wide, f, q, k, v
+    # node features of 4.9e9 values
+    species = torch.arange(n, dtype=torch.int32, device="cuda") % 5
+    table = torch.randn(5, 4096, device="cuda").to(BF16)
+    x = fc.species_embed(species, table, lmax=3)
+    assert torch.equal(x[-7:, :4096], table[species[-7:].long()]) and not x[-7:, 4096:].any()
+    bar = fc.species_embed_vjp(species, x, 5, lmax=3)
+    # 14,000 equal values a species: 8 groups of 16 in a span (at most 16 + 8 roundings), 110 spans over 32 warps
+    # (4 + 5): fewer than 64 roundings of 2^-24 on the way of any
+    close(bar, table.double().cpu() * 14000, 2 ** -18 * table.double().abs().cpu() * 14000)
+
+
 def test_coincident_nodes(fc):
     """Distance 0 between different nodes: no gradient, and no NaN."""
     c = Case([30], None, 2, 2, 16, F32)
