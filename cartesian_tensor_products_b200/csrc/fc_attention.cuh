@@ -27,7 +27,7 @@ struct AttnArgs {
   float2* part_ml;      // forward: [splits][nr H] maximum and sum
   const float2* stat;   // gradient: [nr H] log-sum (base 2), delta
   float4* rowpart;      // gradient: [splits][nr H] position and slope sums
-  float4* rowmean;      // tcgen05 gradient: the same sums of the weights alone, and
+  float4* rowmean;      // 16-bit gradient: the same sums of the weights alone, and
   float* rowrest;       // the row's sum of dt, which an exact delta makes 0
   float4* colpart;      // gradient: [kv_splits][KV][ns] position sums
   int kv_splits;        // parts of the receivers (key and value gradients)

@@ -485,7 +485,7 @@ static int run_dim(bool kv, const AttnArgs& a, cudaStream_t s) {
 // Takes the rest of delta out of a row's sums, parts added: with e = sum dt (the
 // error of delta, as the weights sum to 1), the sums of P (dP - delta) x are
 // those of dt x less e times those of P x.  They go to the first part; delta
-// itself is put right for the sender side.
+// itself is put right for the sender side if stat is given.
 __global__ void __launch_bounds__(256) attn_row_fix_kernel(AttnArgs a, float2* __restrict__ stat) {
   const long long rows = (long long)a.nr * a.H, row = (long long)blockIdx.x * 256 + threadIdx.x;
   if (row >= rows) return;
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(256) attn_row_fix_kernel(AttnArgs a, float2* _
     e += a.rowrest[p * rows + row];
   }
   a.rowpart[row] = make_float4(s.x - e * m.x, s.y - e * m.y, s.z - e * m.z, s.w - e * m.w);
-  stat[row].y += e;
+  if (stat) stat[row].y += e;
 }
 int launch_attn_row_fix(const AttnArgs& a, float2* stat, cudaStream_t s) {
   const long long rows = (long long)a.nr * a.H;

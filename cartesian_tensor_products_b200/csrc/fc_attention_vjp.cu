@@ -52,16 +52,22 @@ struct VjpSmem {
   // Blocks per SM that the registers are held to.  A short structure is one tile
   // per block, whose latency a second block hides: 128 molecules of 9 to 70
   // atoms, 8 heads, gradient in us with one / two: FP32 32-wide 156/115, BF16
-  // 64-wide 128/103 (spills and all).  FP32 64-wide is the other way round on
+  // 64-wide 128/106 (spills and all).  FP32 64-wide is the other way round on
   // long structures (4 of 300 to 900 nodes 601/651; the molecules 233/201).
   static constexpr int blocks = sizeof(T) == 2 || DP <= 32 ? 2 : 1;
-  static_assert(64 * (2 * DP + 3) * sizeof(float) <= tiles && bytes <= 232448, "shared memory");
+  static_assert(64 * (DP + 9) * sizeof(float) <= tiles && 64 * (2 * DP + 3) * sizeof(float) <= tiles && bytes <= 232448, "shared memory");
 };
 
-// Query gradient, receiver position sums and slope sums.
+// Query gradient, receiver position sums and slope sums.  16-bit rows: delta is
+// as exact as a forward with 16-bit weights, dP truncated by the tensor core, and
+// what they miss adds up over a row (4e-6 of a BF16 slope gradient at 49 rows of
+// some 90 senders).  The weights sum to 1, so that e = sum dt is that rest: the
+// sums of P (dP - delta) x are those of dt x less e times those of P x.
 template <class T, int DP>
 __global__ void __launch_bounds__(256, VjpSmem<T, DP>::blocks) attn_vjp_q_kernel(AttnArgs a) {
   constexpr int BN = VjpSmem<T, DP>::BN, BH = BN / 2, NT = BH / 8, S = kStride<T, DP>;
+  constexpr bool Rest = sizeof(T) == 2;
+  constexpr int NS = Rest ? 9 : 4;   // sums of a row: position, slope; of the weights: the same; dt
   extern __shared__ __align__(16) unsigned char smem[];
   T* qs = reinterpret_cast<T*>(smem);
   T* gs = qs + 64 * S;
@@ -122,7 +128,9 @@ __global__ void __launch_bounds__(256, VjpSmem<T, DP>::blocks) attn_vjp_q_kernel
   }
   const float mul = a.cap > 0.0f ? a.scale / a.cap : a.scale * kLog2e;
   const float cap2 = a.cap * kLog2e;
-  float acc[DP / 8][4], bx[2] = {0.f, 0.f}, by[2] = {0.f, 0.f}, bz[2] = {0.f, 0.f}, bs[2] = {0.f, 0.f};
+  float acc[DP / 8][4], sum[NS][2];
+#pragma unroll
+  for (int n = 0; n < NS; ++n) sum[n][0] = sum[n][1] = 0.0f;
 #pragma unroll
   for (int d = 0; d < DP / 8; ++d)
 #pragma unroll
@@ -170,8 +178,14 @@ __global__ void __launch_bounds__(256, VjpSmem<T, DP>::blocks) attn_vjp_q_kernel
           const float dt = f.w != 0.0f ? 0.0f : p * (dp[n][2 * h + c] - delta[h]);
           if (a.pos_r) {
             const float w = dt * inv;
-            bx[h] += w * dx; by[h] += w * dy; bz[h] += w * dz;
-            bs[h] += dt * dist;
+            sum[0][h] += w * dx; sum[1][h] += w * dy; sum[2][h] += w * dz;
+            sum[3][h] += dt * dist;
+            if constexpr (Rest) {
+              const float pw = f.w != 0.0f ? 0.0f : p, wp = pw * inv;
+              sum[4][h] += wp * dx; sum[5][h] += wp * dy; sum[6][h] += wp * dz;
+              sum[7][h] += pw * dist;
+              sum[8][h] += dt;
+            }
           }
           s[n][2 * h + c] = dt * dc;
         }
@@ -182,27 +196,24 @@ __global__ void __launch_bounds__(256, VjpSmem<T, DP>::blocks) attn_vjp_q_kernel
   }
   cp_wait<0>();
   __syncthreads();
-  float* mg = reinterpret_cast<float*>(smem);   // [64] rows of the second half: DP values, four sums
+  float* mg = reinterpret_cast<float*>(smem);   // [64] rows of the second half: DP values, NS sums
 
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      bx[h] += __shfl_xor_sync(0xffffffffu, bx[h], o);
-      by[h] += __shfl_xor_sync(0xffffffffu, by[h], o);
-      bz[h] += __shfl_xor_sync(0xffffffffu, bz[h], o);
-      bs[h] += __shfl_xor_sync(0xffffffffu, bs[h], o);
-    }
-    float* m = mg + (warp * 16 + g + 8 * h) * (DP + 4);
+    for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+      for (int n = 0; n < NS; ++n) sum[n][h] += __shfl_xor_sync(0xffffffffu, sum[n][h], o);
+    float* m = mg + (warp * 16 + g + 8 * h) * (DP + NS);
     if (half == 1) {
 #pragma unroll
       for (int d = 0; d < DP / 8; ++d) {
         m[d * 8 + c2] = acc[d][2 * h];
         m[d * 8 + c2 + 1] = acc[d][2 * h + 1];
       }
-      if ((lane & 3) == 0) {
-        m[DP] = bx[h]; m[DP + 1] = by[h]; m[DP + 2] = bz[h]; m[DP + 3] = bs[h];
-      }
+      if ((lane & 3) == 0)
+#pragma unroll
+        for (int n = 0; n < NS; ++n) m[DP + n] = sum[n][h];
     }
   }
   __syncthreads();
@@ -210,12 +221,23 @@ __global__ void __launch_bounds__(256, VjpSmem<T, DP>::blocks) attn_vjp_q_kernel
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (vr[h] >= at.v1) continue;
-    const float* m = mg + (warp * 16 + g + 8 * h) * (DP + 4);
-    bx[h] += m[DP]; by[h] += m[DP + 1]; bz[h] += m[DP + 2]; bs[h] += m[DP + 3];
+    const float* m = mg + (warp * 16 + g + 8 * h) * (DP + NS);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) sum[n][h] += m[DP + n];
     const long long row = vr[h] / a.G * a.H + kvh * a.G + (int)(vr[h] % a.G);
     const long long pr = (long long)blockIdx.z * a.nr * a.H + row;
-    if (a.rowpart && (lane & 3) == 0)
-      a.rowpart[pr] = make_float4(-sl[h] * bx[h], -sl[h] * by[h], -sl[h] * bz[h], -bs[h]);
+    if (a.rowpart && (lane & 3) == 0) {
+      if constexpr (Rest) {
+        if (a.splits > 1) {   // the row's parts meet in attn_row_fix_kernel
+          a.rowmean[pr] = make_float4(-sl[h] * sum[4][h], -sl[h] * sum[5][h], -sl[h] * sum[6][h], -sum[7][h]);
+          a.rowrest[pr] = sum[8][h];
+        } else {
+#pragma unroll
+          for (int n = 0; n < 4; ++n) sum[n][h] -= sum[8][h] * sum[4 + n][h];
+        }
+      }
+      a.rowpart[pr] = make_float4(-sl[h] * sum[0][h], -sl[h] * sum[1][h], -sl[h] * sum[2][h], -sum[3][h]);
+    }
     if (!a.qb) continue;
 #pragma unroll
     for (int d = 0; d < DP / 8; ++d) {
@@ -501,8 +523,9 @@ static VjpLayout vjp_layout(const fc_attn_desc* d, int B, int nr, int ns) {
   l.stat = 0;
   l.rowpart = round16(rows * sizeof(float2));
   l.rowmean = l.rowpart + rp * sizeof(float4);
-  l.rowrest = l.rowmean + (l.plan.tc_vjp ? rp * sizeof(float4) : 0);
-  l.colpart = l.rowrest + (l.plan.tc_vjp ? round16(rp * sizeof(float)) : 0);
+  const bool rest = l.plan.tc_vjp || (d->dtype != FC_F32 && l.plan.q_splits > 1);
+  l.rowrest = l.rowmean + (rest ? rp * sizeof(float4) : 0);
+  l.colpart = l.rowrest + (rest ? round16(rp * sizeof(float)) : 0);
   l.part = l.colpart + cp * sizeof(float4);
   l.part_k = l.part + pq;
   l.part_v = l.part_k + pk;
@@ -551,8 +574,9 @@ static int run_vjp(int dtype, const AttnArgs& a, const VjpWants& w, bool tc, con
   AttnArgs sums = a;   // as the sums over heads and nodes see it
   if (a.nr > 0 && (a.qb || a.rowpart)) {
     rc = run_side<T>(dtype, tc, false, a, s);
-    if (rc == FC_OK && tc && a.rowpart) {
-      rc = launch_attn_row_fix(a, stat, s);
+    if (rc == FC_OK && a.rowpart && (tc || (sizeof(T) == 2 && a.splits > 1))) {
+      // the strips leave delta as it is: it is what they are given for q_bar too
+      rc = launch_attn_row_fix(a, tc ? stat : nullptr, s);
       sums.splits = 1;
     }
     if (a.qb && a.splits > 1)
