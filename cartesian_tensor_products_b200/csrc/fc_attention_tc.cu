@@ -396,7 +396,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
       __syncwarp();
       if (lane == 0) tc::bar_arrive(&p_full[i & 3]);
     }
-    if (j > 0 && !fail && !tc::bar_wait(&o_full[wg], (j - 1) & 1, lim)) fail = true;
+    // Every product is complete: drain has one phase.  (o_full[wg] has one per tile,
+    // and the product of the tile before last may still be open here, whose
+    // predecessor has the parity of the last.)
+    if (j > 0 && !fail && !tc::bar_wait(drain, 0, lim)) fail = true;
     tc::fence_after_sync();
     if (!set) m = -INFINITY;
     const bool have = j > 0 && !fail;   // else this group's output columns hold nothing

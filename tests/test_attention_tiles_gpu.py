@@ -1,0 +1,34 @@
+"""The tcgen05 attention kernels at every small count of stream tiles of a block (64 rows each), and at counts around
+the depth of their rings, against the plain 64-bit forms.  The senders and receivers are few enough blocks, or many
+enough, that the streamed side is split or is not."""
+import pytest
+import torch
+
+from test_nodes_gpu import BF16, F16, Case, fc  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d,dtype", [(64, BF16), (128, F16)])
+@pytest.mark.parametrize("tiles", [1, 2, 3, 4, 5, 6, 7, 8, 9, 11, 17])
+def test_tile_counts(fc, tiles, d, dtype):  # noqa: F811
+    """96 structures of 128 receivers are more blocks than the card takes at once, so that no structure is split."""
+    send = [64 * tiles - (b % 3) * (31 if tiles > 1 else 0) for b in range(96)]
+    Case([128] * 96, send, 2, 2, d, dtype, cap=5.0, seed=tiles).check(fc)
+
+
+@pytest.mark.parametrize("tiles", [4, 6, 9, 13, 29])
+def test_tile_counts_of_split_structures(fc, tiles):  # noqa: F811
+    """One structure: its senders, and in the gradient its receivers, are shared by several blocks."""
+    Case([64 * tiles - 7], None, 2, 1, 64, BF16, cap=5.0, hide=0.1, seed=tiles).check(fc)
+
+
+def test_many_tiles_repeat_exactly(fc):  # noqa: F811
+    """What reads a product before it is complete reads different values from run to run."""
+    c = Case([2100, 1500], None, 8, 8, 64, BF16, cap=9.0, hide=0.1)
+    first = c.run(fc)
+    for _ in range(30):
+        again = c.run(fc)
+        for a, b in zip([*first[0], *first[1]], [*again[0], *again[1]]):
+            assert a is None or torch.equal(a, b)
+    assert fc.device_error() == 0
