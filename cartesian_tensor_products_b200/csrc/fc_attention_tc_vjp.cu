@@ -385,8 +385,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_vjp_tc_kernel(AttnArgs a, 
       __syncwarp();
       if (lane == 0) tc::bar_arrive(&p_full[b]);
     }
-    // the accumulators are complete when the last tile's products are
-    if (nt > 0 && !fail && !tc::bar_wait(&done[(nt - 1) % NB], ((nt - 1) / NB) & 1, lim)) fail = true;
+    // The accumulators are complete: drain has one phase.  (The last tile's done
+    // barrier has one per tile of its buffer: the group that did not hold that
+    // tile could pass on the phase before last.)
+    if (nt > 0 && !fail && !tc::bar_wait(drain, 0, lim)) fail = true;
     tc::fence_after_sync();
     asm volatile("bar.sync 1, 256;" ::: "memory");
     float* mg = reinterpret_cast<float*>(smem);   // [NS][128]

@@ -101,7 +101,10 @@ def early_waits(tiles, stages, bufs, ahead, outputs, last, seed):
 
 
 FORWARD = dict(bufs=4, ahead=3, outputs="groups")
-PROTOCOLS = {"forward": dict(FORWARD, stages=8), "forward, wide": dict(FORWARD, stages=5)}
+PROTOCOLS = {"forward": dict(FORWARD, stages=8), "forward, wide": dict(FORWARD, stages=5),
+             "gradient": dict(bufs=3, ahead=3, outputs="tiles", stages=6),
+             "gradient, wide": dict(bufs=3, ahead=3, outputs="tiles", stages=4),
+             "key and value gradient, wide": dict(bufs=2, ahead=2, outputs="tiles", stages=4)}
 
 
 @pytest.mark.parametrize("name", list(PROTOCOLS))
