@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
       if (lane == 0) tc::bar_arrive(q_full);
       for (int i = cw; i < nt; i += kAtCopiers) {
         const int s = i % NST, round = i / NST;
-        if (round > 0 && !tc::bar_wait(&freeb[s], (round - 1) & 1, lim)) {
+        if (round > 0 && !tc::warp_wait(&freeb[s], (round - 1) & 1, lim)) {
           fail = true;
           break;
         }
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
           f[3 * kAtStep] = ok ? 0.0f : -INFINITY;
           dead[n] = __ballot_sync(0xffffffffu, !ok);
         }
-        if (!tc::bar_wait(&land[s], round & 1, lim)) {
-          tc::bar_wait(&land[s], round & 1, kAtDrainNs);   // let the copy land
+        if (!tc::warp_wait(&land[s], round & 1, lim)) {
+          tc::warp_wait(&land[s], round & 1, kAtDrainNs);   // let the copy land
           fail = true;
           break;
         }
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
     int j = 0;   // tiles of this group
     for (int i = wg; i < nt; i += 2, ++j) {
       const int s = i % NST;
-      if (!tc::bar_wait(&full[s], (i / NST) & 1, lim) || !tc::bar_wait(&s_full[i & 3], (i >> 2) & 1, lim)) {
+      if (!__all_sync(0xffffffffu, tc::bar_wait(&full[s], (i / NST) & 1, lim) && tc::bar_wait(&s_full[i & 3], (i >> 2) & 1, lim))) {
         fail = true;
         break;
       }
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
           if (j > 0) {   // rescale the sum and the output so far (0 before the row's first score)
             const float al = set ? ex2(-up) : 1.0f;
             l *= al;
-            if (!tc::bar_wait(&o_full[wg], (j - 1) & 1, lim)) {
+            if (!tc::warp_wait(&o_full[wg], (j - 1) & 1, lim)) {
               fail = true;
               break;
             }
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_fwd_tc_kernel(AttnArgs a, 
     // Every product is complete: drain has one phase.  (o_full[wg] has one per tile,
     // and the product of the tile before last may still be open here, whose
     // predecessor has the parity of the last.)
-    if (j > 0 && !fail && !tc::bar_wait(drain, 0, lim)) fail = true;
+    if (j > 0 && !fail && !tc::warp_wait(drain, 0, lim)) fail = true;
     tc::fence_after_sync();
     if (!set) m = -INFINITY;
     const bool have = j > 0 && !fail;   // else this group's output columns hold nothing

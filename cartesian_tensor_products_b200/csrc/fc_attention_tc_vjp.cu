@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_vjp_tc_kernel(AttnArgs a, 
       const uint32_t bytes = (uint32_t)(2 * L::panels * npt * group * 128);
       for (int i = cw; i < nt; i += kAtCopiers) {
         const int s = i % NST, round = i / NST;
-        if (round > 0 && !tc::bar_wait(&freeb[s], (round - 1) & 1, lim)) {
+        if (round > 0 && !tc::warp_wait(&freeb[s], (round - 1) & 1, lim)) {
           fail = true;
           break;
         }
@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_vjp_tc_kernel(AttnArgs a, 
           }
           dead[n] = __ballot_sync(0xffffffffu, !ok && !tail);
         }
-        if (!tc::bar_wait(&land[s], round & 1, lim)) {
-          tc::bar_wait(&land[s], round & 1, kAtDrainNs);   // let the copy land
+        if (!tc::warp_wait(&land[s], round & 1, lim)) {
+          tc::warp_wait(&land[s], round & 1, kAtDrainNs);   // let the copy land
           fail = true;
           break;
         }
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_vjp_tc_kernel(AttnArgs a, 
     bool easy = true;   // the last tile's scores were in the polynomial's range
     for (int i = wg; i < nt; i += 2) {
       const int s = i % NST, b = i % NB;
-      if (!tc::bar_wait(&full[s], (i / NST) & 1, lim) || !tc::bar_wait(&s_full[b], (i / NB) & 1, lim)) {
+      if (!__all_sync(0xffffffffu, tc::bar_wait(&full[s], (i / NST) & 1, lim) && tc::bar_wait(&s_full[b], (i / NB) & 1, lim))) {
         fail = true;
         break;
       }
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_vjp_tc_kernel(AttnArgs a, 
     // The accumulators are complete: drain has one phase.  (The last tile's done
     // barrier has one per tile of its buffer: the group that did not hold that
     // tile could pass on the phase before last.)
-    if (nt > 0 && !fail && !tc::bar_wait(drain, 0, lim)) fail = true;
+    if (nt > 0 && !fail && !tc::warp_wait(drain, 0, lim)) fail = true;
     tc::fence_after_sync();
     asm volatile("bar.sync 1, 256;" ::: "memory");
     float* mg = reinterpret_cast<float*>(smem);   // [NS][128]

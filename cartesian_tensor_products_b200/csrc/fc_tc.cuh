@@ -126,6 +126,14 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint64_
   }
 }
 
+// The same by a whole (converged) warp, with one answer for all its lanes: each
+// polls and times by itself, and where one gives up all do.  Whatever is
+// collective behind a wait (votes, shuffles, tensor-memory loads and stores)
+// needs that: lanes that went two ways would wait for each other for good.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, limit_ns));
+}
+
 // Arrival that also expects `bytes` of asynchronous-copy data on the barrier.
 __device__ __forceinline__ void bar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
