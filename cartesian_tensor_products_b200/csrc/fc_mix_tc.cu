@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ladder_mix_tc_kernel(Geom geo,
       const int R = geo.N * w;
       const int row0 = (t - tile_first(geo, l)) * kTcRows;
       const uint32_t d_tmem = tmem + (uint32_t)(ti & 1) * kTcRows + ((uint32_t)(32 * ew) << 16);
-      if (!tc::bar_wait(&acc_full[ti & 1], (ti >> 1) & 1, lim)) {
+      if (!tc::warp_wait(&acc_full[ti & 1], (ti >> 1) & 1, lim)) {
         fail = true;
         break;
       }
@@ -669,8 +669,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) path_mix_tc_kernel(PathGeom geo
       const int kc = pg_kc(geo, l);
       for (int c = 0; c < kc; ++c, ++g) {
         const int s = g % kTcStages, b = g & 1;
-        if (!tc::bar_wait(&stage_full[s], (g / kTcStages) & 1, lim) ||
-            (g >= 2 && !tc::bar_wait(&cvt_free[b], ((g - 2) >> 1) & 1, lim))) {
+        if (!tc::warp_wait(&stage_full[s], (g / kTcStages) & 1, lim) ||
+            (g >= 2 && !tc::warp_wait(&cvt_free[b], ((g - 2) >> 1) & 1, lim))) {
           fail = true;
           break;
         }
@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) path_mix_tc_kernel(PathGeom geo
       const size_t step = (size_t)geo.orow * kTcC;
       const int nr = min(kTcRows, geo.N - cmn);
       for (int gi = 0; gi < ng; ++gi, ++h) {
-        if (!tc::bar_wait(&acc_full[h & 1], (h >> 1) & 1, lim)) {
+        if (!tc::warp_wait(&acc_full[h & 1], (h >> 1) & 1, lim)) {
           fail = true;
           break;
         }
@@ -978,7 +978,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) rows_wgrad_tc_kernel(WgGeom geo
       wg_chunk(geo, ch, l, e, q);
       const int kv = wg_nodes(l) * (2 * l + 1);   // stage rows the loads wrote
       const int s = g % kRwStages, bb = g % kRwBufs;
-      if (!tc::bar_wait(&stage_full[s], (g / kRwStages) & 1, lim)) {
+      if (!tc::warp_wait(&stage_full[s], (g / kRwStages) & 1, lim)) {
         fail = true;
         break;
       }
@@ -992,7 +992,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) rows_wgrad_tc_kernel(WgGeom geo
         if (r >= kv) v[r] = 0.0f;
       __syncwarp();   // the stage's values are in registers: release it
       if (lane == 0) tc::bar_arrive(&stage_free[s]);
-      if (g >= kRwBufs && !tc::bar_wait(&cvt_free[bb], ((g / kRwBufs) - 1) & 1, lim)) {
+      if (g >= kRwBufs && !tc::warp_wait(&cvt_free[bb], ((g / kRwBufs) - 1) & 1, lim)) {
         fail = true;
         break;
       }
@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(kRwThreads, 1) rows_wgrad_tc_kernel(WgGeom geo
       if (ch < c_end) wg_chunk(geo, ch, l, e, q);
       const bool fresh = ch == c_end || l != pl || e != pe || run == kRwSeg;
       if (fresh && h >= 0) {   // segment h (rank pl, map pe) is complete: add it
-        if (!tc::bar_wait(&acc_full[h & 1], (h >> 1) & 1, lim)) {
+        if (!tc::warp_wait(&acc_full[h & 1], (h >> 1) & 1, lim)) {
           fail = true;
           break;
         }
