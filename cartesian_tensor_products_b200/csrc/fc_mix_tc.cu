@@ -266,12 +266,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) ladder_mix_tc_kernel(Geom geo,
                         kTcBlockFloats * sizeof(float), &stage_full[s]);
         }
       }
-      if (fail) {
-        // let the copies already issued land before the CTA can exit
-        for (int k = 1; k <= kTcStages && g - k >= 0; ++k)
-          tc::bar_wait(&stage_full[(g - k) % kTcStages], ((g - k) / kTcStages) & 1, kTcDrainNs);
-        if (w_loads > 0) tc::bar_wait(w_full, (w_loads - 1) & 1, kTcDrainNs);
-      }
+      // The copies issued land before the CTA can exit.  Also where this role never
+      // had to wait: another one may have given up on them.
+      for (int k = 1; k <= kTcStages && g - k >= 0; ++k)
+        if (!tc::bar_wait(&stage_full[(g - k) % kTcStages], ((g - k) / kTcStages) & 1, kTcDrainNs)) fail = true;
+      if (w_loads > 0 && !tc::bar_wait(w_full, (w_loads - 1) & 1, kTcDrainNs)) fail = true;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -602,9 +601,9 @@ __global__ void __launch_bounds__(kPmThreads, 1) path_mix_tc_kernel(PathGeom geo
           tc::bulk_load(dst + 2 * kTcBlockFloats, wt + lo + co, kB, &stage_full[s]);
         }
       }
-      if (fail)   // let the copies already issued land
-        for (int k = 1; k <= kTcStages && g - k >= 0; ++k)
-          tc::bar_wait(&stage_full[(g - k) % kTcStages], ((g - k) / kTcStages) & 1, kTcDrainNs);
+      // the copies issued land before the CTA can exit, whichever role gave up
+      for (int k = 1; k <= kTcStages && g - k >= 0; ++k)
+        if (!tc::bar_wait(&stage_full[(g - k) % kTcStages], ((g - k) / kTcStages) & 1, kTcDrainNs)) fail = true;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -904,9 +903,9 @@ __global__ void __launch_bounds__(kRwThreads, 1) rows_wgrad_tc_kernel(WgGeom geo
         tc::tma_load_4d(dst + kRwRowFloats, &maps.b[l], 0, e, 0, q * nn, &stage_full[s]);
       }
     }
-    if (fail && lane == 0)   // let the copies already issued land
+    if (lane == 0)   // the copies issued land before the CTA can exit, whichever role gave up
       for (int k = 1; k <= kRwStages && g - k >= 0; ++k)
-        tc::bar_wait(&stage_full[(g - k) % kRwStages], ((g - k) / kRwStages) & 1, kTcDrainNs);
+        if (!tc::bar_wait(&stage_full[(g - k) % kRwStages], ((g - k) / kRwStages) & 1, kTcDrainNs)) fail = true;
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------

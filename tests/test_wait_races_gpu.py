@@ -4,6 +4,7 @@ the right results.  With the default bound back, so does every call."""
 import pytest
 import torch
 
+from cartesian_tensor_products_b200 import workloads as W
 from test_nodes_gpu import BF16, F16, Case, fc  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -43,4 +44,33 @@ def test_attention_waits_race_their_limit(fc, d, kv, dtype):  # noqa: F811
     def call():
         outs, bars = c.run(fc)
         return [t for t in (*outs, *bars) if t is not None]
+    assert race(fc, call) > 0
+
+
+@pytest.mark.parametrize("nodes", [20, 600])
+def test_ladder_waits_race_their_limit(fc, nodes):  # noqa: F811
+    """20 nodes: blocks whose copies all fit the stages, so that the copying role itself has nothing to wait for when
+    another gives up.  The weight gradients are summed by atomic additions, so that only the rest is bit-equal."""
+    L, C, order = 3, 128, 3
+    lad = W.ladder_inputs(nodes, L, C, order, 23)
+    A1, pw, mw, gz = (torch.from_numpy(lad[k]).cuda() for k in ("A1", "path_w", "mix_w", "gz"))
+
+    def call():
+        states, z = fc.product_ladder(L, order, A1, pw, mw)
+        a1b = fc.product_ladder_vjp(L, order, A1, pw, mw, states, gz)[0]
+        return [states, z, a1b]
+    assert race(fc, call) > 0
+
+
+@pytest.mark.parametrize("nodes", [8, 300])
+def test_full_ladder_waits_race_their_limit(fc, nodes):  # noqa: F811
+    L, C, order = 2, 128, 3
+    fl = W.full_ladder_inputs(nodes, L, C, order, 12)
+    A, W1, Wq = (torch.from_numpy(fl[k]).cuda() for k in ("A", "W1", "Wq"))
+    gz = torch.randn_like(fc.full_ladder(L, order, A, W1, Wq)[1])
+
+    def call():
+        states, z = fc.full_ladder(L, order, A, W1, Wq)
+        a_bar = fc.full_ladder_vjp(L, order, A, W1, Wq, states, gz)[0]
+        return [states, z, a_bar]
     assert race(fc, call) > 0
