@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a) {
 
 int check_attn(const fc_attn_desc* d, int n_struct, int n_recv, int n_send) {
   if (!d || !row_dtype(d->dtype) || n_struct < 0 || n_recv < 0 || n_send < 0) return FC_ERR_ARG;
+  if (n_struct > kMaxStruct) return FC_ERR_ARG;
   if (d->heads < 1 || d->kv_heads < 1 || d->heads > 1024 || d->kv_heads > d->heads || d->heads % d->kv_heads)
     return FC_ERR_ARG;
   if (d->head_dim < 8 || d->head_dim > 128) return FC_ERR_ARG;

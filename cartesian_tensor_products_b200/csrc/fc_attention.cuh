@@ -118,6 +118,7 @@ __device__ __forceinline__ void strip_tanh(float (&s)[NT][4], float mul) {
 // other side.  Structure b owns the tile numbers from
 // floor(start_b mult / tile) + b on; these ranges are disjoint, so that the
 // structure follows from a search in ptr alone.  Every lane of a warp calls.
+constexpr int kMaxStruct = INT32_MAX - 64;   // the search looks up to 31 past structure B + 1
 struct TileAt {
   int b;               // structure, 0 .. B + 1
   long long v0, v1;    // virtual rows from the tile's first to the structure's end

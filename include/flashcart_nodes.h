@@ -104,8 +104,8 @@ int fc_head_norm_rotate_vjp(const fc_head_desc *desc, int n_nodes, const void *x
                             float *gamma_q_bar, float *gamma_k_bar, float *pos_bar,
                             void *workspace, size_t ws_bytes, fc_stream_t stream);
 
-/* Attention descriptor.  heads is a multiple of kv_heads: receiver head h
- * reads key and value head h / (heads / kv_heads). */
+/* Attention descriptor.  heads (at most 1024) is a multiple of kv_heads:
+ * receiver head h reads key and value head h / (heads / kv_heads). */
 typedef struct {
   int dtype;
   int heads;
@@ -121,7 +121,8 @@ typedef struct {
  *   out_i = sum_j exp(t_ij - lse_i) v_j,  lse_i = log sum_j exp(t_ij)
  * Structure b holds receivers recv_ptr[b] .. recv_ptr[b+1] - 1 and senders
  * send_ptr[b] .. send_ptr[b+1] - 1 (int32 [n_struct + 1] on the device,
- * non-decreasing; either side of a structure may be empty).  Receivers and
+ * non-decreasing; either side of a structure may be empty; n_struct at most
+ * 2^31 - 65).  Receivers and
  * senders are counted apart, as in fc_edge_conv_rect: the same pointer twice
  * is self-attention, a few receivers against many senders is a probe, and a
  * receiver range of a graph cut over several GPUs attends to the gathered
