@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(32 * WM * WN) attn_strip_kernel(AttnArgs a) {
   const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, wm = (tid >> 5) % WM, wn = (tid >> 5) / WM;
   int slo, shi;
   other_side(a.send_ptr, a.B, a.ns, at.b, slo, shi);
-  const int all = shi > slo ? (shi - slo + BN - 1) / BN : 0;
-  const int t0 = (int)((long long)all * blockIdx.z / a.splits), t1 = (int)((long long)all * (blockIdx.z + 1) / a.splits);
+  const long long all = shi > slo ? ((long long)shi - slo + BN - 1) / BN : 0;
+  const int t0 = (int)(all * blockIdx.z / a.splits), t1 = (int)(all * (blockIdx.z + 1) / a.splits);
   const T* q = static_cast<const T*>(a.q);
   const T* k = static_cast<const T*>(a.k) + (long long)kvh * a.D;
   const T* v = static_cast<const T*>(a.v) + (long long)kvh * a.D;
@@ -314,7 +314,8 @@ AttnPlan attn_plan(const fc_attn_desc* d, int B, int nr, int ns) {
   const int G = d->heads / d->kv_heads, KV = d->kv_heads, sms = device_sm_count();
   const long long rows = (long long)nr * G, per_r = B > 0 ? rows / B : 0, per_s = B > 0 ? ns / B : 0;
   const int step = d->dtype == FC_F32 && d->head_dim > 64 ? 32 : 64;
-  const bool can = d->dtype != FC_F32 && per_s >= 64 && rows < (1ll << 31);
+  // (rows and the end of a tensor copy's box past the last sender fit 31 bits)
+  const bool can = d->dtype != FC_F32 && per_s >= 64 && rows <= INT32_MAX - 64 && ns <= INT32_MAX - 64;
   p.tc = can && per_r >= tc_rows(d->head_dim, false);
   p.tc_vjp = can && per_r >= tc_rows(d->head_dim, true) && G <= 64;
   // few: up to two 16-row tiles a structure

@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(256, VjpSmem<T, DP>::blocks) attn_vjp_q_kernel
   const int kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) & 3, half = tid >> 7;
   int slo, shi;
   other_side(a.send_ptr, a.B, a.ns, at.b, slo, shi);
-  const int all = shi > slo ? (shi - slo + BN - 1) / BN : 0;
-  const int t0 = (int)((long long)all * blockIdx.z / a.splits), t1 = (int)((long long)all * (blockIdx.z + 1) / a.splits);
+  const long long all = shi > slo ? ((long long)shi - slo + BN - 1) / BN : 0;
+  const int t0 = (int)(all * blockIdx.z / a.splits), t1 = (int)(all * (blockIdx.z + 1) / a.splits);
   const T* k = static_cast<const T*>(a.k) + (long long)kvh * a.D;
   const T* v = static_cast<const T*>(a.v) + (long long)kvh * a.D;
   auto rowat = [&](const T* base, long long ld, int r) {

@@ -1,0 +1,38 @@
+"""The node operators at the ends of their ranges."""
+import pytest
+import torch
+
+from parity import FWD_TOL, VJP_TOL
+from test_nodes_gpu import BF16, close, fc  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def test_senders_to_the_last_of_31_bits(fc):  # noqa: F811
+    """One receiver against 2^31 - 1 senders (34 GB of rows): the last two hold nearly all of the weight.  The count
+    of their tiles of 64 does not fit 32 bits ahead of its division."""
+    n, d = 2 ** 31 - 1, 8
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of free device memory")
+    k = torch.zeros(n, 1, d, dtype=BF16, device="cuda")
+    k[-2:, 0, :2] = torch.tensor([[40.0, 1.0], [40.5, 0.0]], dtype=BF16, device="cuda")
+    q = torch.zeros(1, 1, d, dtype=BF16, device="cuda")
+    q[0, 0, 0] = 1.0
+    g = torch.ones_like(q)
+    ends = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    out, lse, o32 = fc.node_attention(q, k, k, *ends, scale=1.0, residual=True)
+    t = torch.tensor([40.0, 40.5], dtype=torch.float64)
+    z = torch.log(torch.exp(t).sum() + float(n - 2))
+    p = torch.exp(t - z)
+    rows = k[-2:, 0].double().cpu()
+    ref = (p[:, None] * rows).sum(0)
+    close(lse, z.reshape(1, 1), FWD_TOL * float(z))
+    # the weights as two 16-bit terms
+    close(o32, ref.reshape(1, 1, d), FWD_TOL * float(ref.abs().max()) + 2.0 ** -16 * ref.abs().reshape(1, 1, d))
+    qb = fc.node_attention_vjp(q, k, k, o32, lse, g, *ends, scale=1.0, want=("q",))[0]
+    dp = rows.sum(1)
+    ds = p * (dp - ref.sum())     # and P (0 - sum of ref) for the rest, times keys of 0
+    want = (ds[:, None] * rows).sum(0)
+    # dS rounded to 16 bits: 2^-8 of |dS| |k|; delta, off by its 2^-16 of sum P |v| (41), moves dS by P of that; then one rounding
+    bound = 2.0 ** -8 * ((ds.abs()[:, None] * rows.abs()).sum(0) + want.abs()) + 41 * 2.0 ** -16 * 1.1 * (p[:, None] * rows.abs()).sum(0)
+    close(qb, want.reshape(1, 1, d), (bound + VJP_TOL * float(want.abs().max())).reshape(1, 1, d))
