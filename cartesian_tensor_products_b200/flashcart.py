@@ -10,6 +10,7 @@ Conventions (layouts, path order, component order) are those of the header.
 """
 import ctypes as ct
 import functools
+import operator
 import os
 
 import torch
@@ -662,7 +663,7 @@ def species_embed_vjp(species, g, n_species, lmax=0, scale=1.0, workspace=None, 
     N, C = species.shape[0], g.shape[1] // NY
     _counts(N, C)
     bar = torch.empty((n_species, C), dtype=_F32, device=index)
-    need = _scratch_size(index, "fc_species_embed_vjp_workspace_size", None, N, n_species, C)
+    need = _scratch_size(index, "fc_species_embed_vjp_workspace_size", None, N, operator.index(n_species), C)
     workspace, ws, size = _bytes(workspace, need, index)
     _check(_lib.fc_species_embed_vjp(dtype, N, n_species, lmax, C, scale,
                                      _on(species, _I32, "species", index, (N,)),
@@ -672,8 +673,14 @@ def species_embed_vjp(species, g, n_species, lmax=0, scale=1.0, workspace=None, 
 
 
 @functools.lru_cache(maxsize=256)
-def _head_desc(*fields):
+def _head_desc_of(*fields):
     return HeadDesc(*fields)
+
+
+def _head_desc(dtype, heads_q, heads_k, head_dim, pairs, eps):
+    """Descriptor of these values.  They are looked up as plain numbers: a tensor of one element would be found by
+    its identity, whatever it holds by then."""
+    return _head_desc_of(dtype, operator.index(heads_q), operator.index(heads_k), head_dim, pairs, float(eps))
 
 
 def _head_args(x, heads_q, gamma_q, gamma_k, pos, freq, eps):
@@ -730,8 +737,12 @@ def head_norm_rotate_vjp(x, g, heads_q, gamma_q=None, gamma_k=None, pos=None, fr
 
 
 @functools.lru_cache(maxsize=256)
-def _attn_desc(*fields):
+def _attn_desc_of(*fields):
     return AttnDesc(*fields)
+
+
+def _attn_desc(dtype, heads, kv_heads, head_dim, scale, cap):
+    return _attn_desc_of(dtype, heads, kv_heads, head_dim, float(scale), float(cap))
 
 
 def _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask, scale, cap):

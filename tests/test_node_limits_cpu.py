@@ -1,5 +1,6 @@
 """Limits of the node operators that are decided on the host."""
 import pytest
+import torch
 
 from test_nodes_cpu import ARG, attn, fc  # noqa: F401
 
@@ -9,3 +10,18 @@ def test_attention_refuses_structures_that_the_tile_search_cannot_count(fc, vjp)
     """The search for a tile's structure looks up to 31 places past n_struct + 1 in 32 bits."""
     for b in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 3, 2 ** 31 - 64):
         assert attn(fc, vjp, b=b) == ARG, b
+
+
+def test_factors_in_tensors_are_read_at_every_call(fc):  # noqa: F811
+    """Descriptors are kept by their values; a tensor of one element that is changed in place is another value."""
+    for make, name in ((lambda t: fc._attn_desc(0, 1, 1, 8, t, 0.0), "scale"), (lambda t: fc._attn_desc(0, 1, 1, 8, 1.0, t), "cap"),
+                       (lambda t: fc._head_desc(0, 1, 1, 8, 0, t), "eps")):
+        t = torch.tensor(0.5)
+        assert getattr(make(t), name) == 0.5
+        t.mul_(4)
+        assert getattr(make(t), name) == 2.0
+        assert make(0.25) is make(0.25)
+    t = torch.tensor(1)
+    assert fc._head_desc(0, t, 1, 8, 0, 1.0).heads_q == 1
+    t.add_(2)
+    assert fc._head_desc(0, t, 1, 8, 0, 1.0).heads_q == 3

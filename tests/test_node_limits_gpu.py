@@ -36,3 +36,17 @@ def test_senders_to_the_last_of_31_bits(fc):  # noqa: F811
     # dS rounded to 16 bits: 2^-8 of |dS| |k|; delta, off by its 2^-16 of sum P |v| (41), moves dS by P of that; then one rounding
     bound = 2.0 ** -8 * ((ds.abs()[:, None] * rows.abs()).sum(0) + want.abs()) + 41 * 2.0 ** -16 * 1.1 * (p[:, None] * rows.abs()).sum(0)
     close(qb, want.reshape(1, 1, d), (bound + VJP_TOL * float(want.abs().max())).reshape(1, 1, d))
+
+
+def test_scale_cap_and_eps_in_tensors_changed_in_place(fc):  # noqa: F811
+    q = torch.randn(20, 2, 16, device="cuda")
+    ptr = torch.tensor([0, 20], dtype=torch.int32, device="cuda")
+    scale, cap, eps = torch.tensor(0.5), torch.tensor(4.0), torch.tensor(1e-6)
+    for _ in range(3):
+        a = fc.node_attention(q, q, q, ptr, scale=scale, cap=cap)
+        b = fc.node_attention(q, q, q, ptr, scale=scale.item(), cap=cap.item())
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        assert torch.equal(fc.head_norm_rotate(q, 1, eps=eps), fc.head_norm_rotate(q, 1, eps=eps.item()))
+        scale.mul_(1.5)
+        cap.mul_(0.5)
+        eps.mul_(1e3)
