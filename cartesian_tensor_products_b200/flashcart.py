@@ -10,6 +10,7 @@ Conventions (layouts, path order, component order) are those of the header.
 """
 import ctypes as ct
 import functools
+import inspect
 import operator
 import os
 
@@ -538,17 +539,20 @@ def _node_op(f):
     """Runs a node operator on its first tensor's device and on `stream` (None:
     that device's current stream), which f gets as the raw handle.  Outputs and
     scratch are allocated on the stream that uses them."""
+    name = next(iter(inspect.signature(f).parameters))
+
     @functools.wraps(f)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError("%s takes CUDA tensors" % f.__name__)
         index = first.get_device()
         if stream is None and index == torch._C._cuda_getDevice():
-            return f(first, *args, stream=torch._C._cuda_getCurrentRawStream(index), **kw)
+            return f(*args, stream=torch._C._cuda_getCurrentRawStream(index), **kw)
         if stream is not None and stream.device.index != index:
             raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, first.device))
         with torch.cuda.device(index), torch.cuda.stream(stream):
-            return f(first, *args, stream=torch._C._cuda_getCurrentRawStream(index), **kw)
+            return f(*args, stream=torch._C._cuda_getCurrentRawStream(index), **kw)
     return call
 
 

@@ -25,3 +25,16 @@ def test_factors_in_tensors_are_read_at_every_call(fc):  # noqa: F811
     assert fc._head_desc(0, t, 1, 8, 0, 1.0).heads_q == 1
     t.add_(2)
     assert fc._head_desc(0, t, 1, 8, 0, 1.0).heads_q == 3
+
+
+def test_every_argument_can_be_named(fc):  # noqa: F811
+    """Also the first: the call gets as far as finding that its tensors are on the CPU."""
+    x, i = torch.zeros(4, 3, 8), torch.zeros(4, dtype=torch.int32)
+    for f, kw in ((fc.species_embed, dict(species=i, table=x[0])), (fc.species_embed_vjp, dict(species=i, g=x[:, 0], n_species=3)),
+                  (fc.head_norm_rotate, dict(x=x, heads_q=2)), (fc.head_norm_rotate_vjp, dict(x=x, g=x, heads_q=2)),
+                  (fc.node_attention, dict(q=x, k=x, v=x, recv_ptr=i)),
+                  (fc.node_attention_vjp, dict(q=x, k=x, v=x, out_f32=x, lse=x[0], g=x, recv_ptr=i))):
+        with pytest.raises(TypeError, match="takes CUDA tensors"):
+            f(**kw)
+    with pytest.raises(TypeError):
+        fc.head_norm_rotate()

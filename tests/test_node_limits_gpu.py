@@ -50,3 +50,22 @@ def test_scale_cap_and_eps_in_tensors_changed_in_place(fc):  # noqa: F811
         scale.mul_(1.5)
         cap.mul_(0.5)
         eps.mul_(1e3)
+
+
+def test_calls_by_name_alone(fc):  # noqa: F811
+    x = torch.randn(20, 4, 16, device="cuda")
+    q, k = x[:, :2], x[:, 2:]
+    ptr = torch.tensor([0, 20], dtype=torch.int32, device="cuda")
+    species = torch.arange(20, dtype=torch.int32, device="cuda") % 3
+    table = torch.randn(3, 8, device="cuda")
+    same = lambda a, b: all(torch.equal(u, v) for u, v in zip(a, b) if u is not None)  # noqa: E731
+    assert torch.equal(fc.species_embed(table=table, species=species), fc.species_embed(species, table))
+    g = torch.randn(20, 8, device="cuda")
+    assert torch.equal(fc.species_embed_vjp(n_species=3, g=g, species=species), fc.species_embed_vjp(species, g, 3))
+    y = fc.head_norm_rotate(heads_q=2, x=x, stream=torch.cuda.current_stream())
+    assert torch.equal(y, fc.head_norm_rotate(x, 2))
+    assert same(fc.head_norm_rotate_vjp(g=y, heads_q=2, x=x), fc.head_norm_rotate_vjp(x, y, 2))
+    out = fc.node_attention(recv_ptr=ptr, v=k, k=k, q=q, residual=True)
+    assert same(out, fc.node_attention(q, k, k, ptr, residual=True))
+    a = (q, k, k, out[2], out[1], q, ptr)
+    assert same(fc.node_attention_vjp(**dict(zip(("q", "k", "v", "out_f32", "lse", "g", "recv_ptr"), a))), fc.node_attention_vjp(*a))
