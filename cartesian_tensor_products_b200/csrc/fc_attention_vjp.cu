@@ -666,9 +666,12 @@ int fc_node_attention_vjp(const fc_attn_desc* desc, int n_struct, int n_recv, in
   a.part_k = reinterpret_cast<float*>(ws + l.part_k);
   a.part_v = reinterpret_cast<float*>(ws + l.part_v);
   a.stat = stat;
-  // the tcgen05 kernels put delta right for the senders' position sums too
+  // With a bias the tcgen05 kernels put delta right for the senders' side from the
+  // row sums of the query gradient's kernel, which therefore runs for k_bar too:
+  // what a gradient holds does not depend on which others are asked for.
   const bool tc = l.plan.tc_vjp && n_recv > 0 && n_send > 0;   // the tensor maps need rows on both sides
-  a.rowpart = pos_recv_bar || slope_bar || (tc && pos_send_bar) ? reinterpret_cast<float4*>(ws + l.rowpart) : nullptr;
+  const bool fix = tc && pos_recv && (k_bar || pos_send_bar);
+  a.rowpart = pos_recv_bar || slope_bar || fix ? reinterpret_cast<float4*>(ws + l.rowpart) : nullptr;
   a.rowmean = reinterpret_cast<float4*>(ws + l.rowmean);
   a.rowrest = reinterpret_cast<float*>(ws + l.rowrest);
   a.colpart = pos_send_bar || (w.self && pos_recv_bar) ? reinterpret_cast<float4*>(ws + l.colpart) : nullptr;

@@ -166,8 +166,8 @@ int fc_node_attention(const fc_attn_desc *desc, int n_struct, int n_recv, int n_
  *   out itself if its rows are packed, ldo = heads * head_dim); g the gradient
  *   of out (step ldg); lse itself takes no gradient.
  *   q_bar, k_bar, v_bar packed ([n][heads][head_dim], rows' type), slope_bar
- *   [heads], pos_*_bar [n][3]: each may be NULL to skip it.  Hidden senders
- *   get 0.  16-bit types round P and ds / scale to the rows' type ahead of the
+ *   [heads], pos_*_bar [n][3]: each may be NULL to skip it, which changes no
+ *   bit of the others.  Hidden senders get 0.  16-bit types round P and ds / scale to the rows' type ahead of the
  *   products; FP16 then has 6e-8 as its smallest step and 65504 as its largest
  *   value, so that g should be scaled (as FP16 losses are) to keep P (g.v)
  *   between them.  Slopes and positions do not pass through 16 bits.

@@ -32,3 +32,21 @@ def test_many_tiles_repeat_exactly(fc):  # noqa: F811
         for a, b in zip([*first[0], *first[1]], [*again[0], *again[1]]):
             assert a is None or torch.equal(a, b)
     assert fc.device_error() == 0
+
+
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("apart", [False, True])
+def test_a_gradient_does_not_depend_on_the_others_asked_for(fc, apart, bias):  # noqa: F811
+    recv = [330, 150]
+    c = Case(recv, [200, 410] if apart else None, 4, 2, 64, BF16, cap=6.0, bias=bias, hide=0.1)
+    (out, lse, o32), bars = c.run(fc)
+    q, k, v = c.parts(c.qw.cuda(), c.kw.cuda())
+    move = lambda t: None if t is None else t.cuda()  # noqa: E731
+    kw = dict(c.kwargs(move), send_ptr=c.sp.cuda(), send_mask=c.mask.cuda())
+    names = ("q", "k", "v", "pos", "pos_send", "slope")
+    for want in (("q",), ("k",), ("v",), ("k", "v"), ("q", "k"), ("pos",), ("slope",), ("k", "slope"), ("v", "pos"), ("q", "v", "slope")):
+        got = fc.node_attention_vjp(q, k, v, o32, lse, c.g.cuda(), c.rp.cuda(), want=want, **kw)
+        for n, a, b in zip(names, got, bars):
+            asked = n in want or n == "pos_send" and "pos" in want
+            assert (a is None) == (b is None or not asked), (want, n)
+            assert a is None or torch.equal(a, b), (want, n)
