@@ -381,6 +381,12 @@ size_t fc_node_attention_workspace_size(const fc_attn_desc* desc, int n_struct, 
   return round16(rows * desc->head_dim * sizeof(float)) + round16(rows * sizeof(float2));
 }
 
+int fc_node_attention_on_tcgen05(const fc_attn_desc* desc, int n_struct, int n_recv, int n_send, int vjp) {
+  if (check_attn(desc, n_struct, n_recv, n_send) != FC_OK) return -1;
+  const AttnPlan plan = attn_plan(desc, n_struct, n_recv, n_send);
+  return n_recv > 0 && n_send > 0 && (vjp ? plan.tc_vjp : plan.tc);
+}
+
 int fc_node_attention(const fc_attn_desc* desc, int n_struct, int n_recv, int n_send, const int32_t* recv_ptr,
                       const int32_t* send_ptr, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
                       int64_t ldv, const float* pos_recv, const float* pos_send, const float* slope,

@@ -115,6 +115,7 @@ _SIGS = {
                                            ct.c_int64] + [_vp] * 5 + [ct.c_int64] + [_vp] * 4
                                 + [ct.c_size_t, _vp]),
     "fc_node_attention_workspace_size": (ct.c_size_t, [ct.POINTER(AttnDesc)] + [ct.c_int] * 3),
+    "fc_node_attention_on_tcgen05": (ct.c_int, [ct.POINTER(AttnDesc)] + [ct.c_int] * 4),
     "fc_node_attention": (ct.c_int, [ct.POINTER(AttnDesc)] + [ct.c_int] * 3 + [_vp] * 2
                           + [_vp, ct.c_int64] * 3 + [_vp] * 4 + [_vp, ct.c_int64] + [_vp] * 3
                           + [ct.c_size_t, _vp]),
@@ -774,6 +775,19 @@ def _attn_args(q, k, v, recv_ptr, send_ptr, pos, pos_send, slope, send_mask, sca
             _on(send_mask, _U8, "send_mask", index, (ns,)))
     d = _attn_desc(dtype, H, KV, D, D ** -0.5 if scale is None else scale, cap)
     return index, d, (B1 - 1, nr, ns), args
+
+
+def node_attention_on_tcgen05(dtype, heads, kv_heads, head_dim, n_struct, n_recv, n_send, vjp=False):
+    """Whether node_attention (or its VJP) of these sizes runs on the tcgen05
+    kernels, whose bounded waits device_error() reports."""
+    if dtype not in _ROW_DTYPES:
+        raise TypeError("rows are float32, bfloat16 or float16, got %s" % (dtype,))
+    _counts(heads, kv_heads, head_dim, n_struct, n_recv, n_send)
+    d = _attn_desc(_ROW_DTYPES[dtype], heads, kv_heads, head_dim, 1.0, 0.0)
+    on = _lib.fc_node_attention_on_tcgen05(d, n_struct, n_recv, n_send, int(vjp))
+    if on < 0:
+        raise ValueError("node_attention takes no such sizes")
+    return on == 1
 
 
 @_node_op

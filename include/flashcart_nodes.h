@@ -153,6 +153,13 @@ int fc_node_attention(const fc_attn_desc *desc, int n_struct, int n_recv, int n_
                       const uint8_t *send_mask, void *out, int64_t ldo, float *lse, float *out_f32,
                       void *workspace, size_t ws_bytes, fc_stream_t stream);
 
+/* Host query: whether fc_node_attention (vjp 0) or its VJP (vjp not 0) runs on
+ * the tcgen05 kernels, whose waits are bounded (fc_device_error): 1 or 0, and
+ * -1 for a descriptor or sizes that the call refuses.  16-bit rows do from some
+ * tens (wide heads) to hundreds (narrow heads) of rows of a structure on; a
+ * call has one kernel, chosen by its average structure. */
+int fc_node_attention_on_tcgen05(const fc_attn_desc *desc, int n_struct, int n_recv, int n_send, int vjp);
+
 /* VJP of fc_node_attention.  With P_ij = exp(t_ij - lse_i), dt_ij =
  * P_ij (g_i.v_j - g_i.out_i) and ds_ij = scale (1 - tanh^2) dt_ij:
  *   q_bar_i = sum_j ds_ij k_j      k_bar_j = sum_{i, heads of the group} ds_ij q_i

@@ -38,3 +38,22 @@ def test_every_argument_can_be_named(fc):  # noqa: F811
             f(**kw)
     with pytest.raises(TypeError):
         fc.head_norm_rotate()
+
+
+def test_which_kernels_a_call_runs_on(fc):  # noqa: F811
+    on = fc.node_attention_on_tcgen05
+    bf16 = torch.bfloat16
+    for vjp in (False, True):
+        assert on(bf16, 4, 4, 64, 2, 600, 600, vjp) and on(torch.float16, 4, 1, 128, 1, 100, 100, vjp)
+        assert not on(torch.float32, 4, 4, 64, 2, 600, 600, vjp)      # FP32 rows: strips
+        assert not on(bf16, 4, 4, 64, 100, 600, 600, vjp)             # short structures
+        assert not on(bf16, 4, 4, 64, 2, 600, 100, vjp)               # fewer than 64 senders
+        assert not on(bf16, 4, 4, 64, 2, 0, 600, vjp) and not on(bf16, 4, 4, 64, 0, 600, 600, vjp)
+        assert on(bf16, 1, 1, 8, 1, 2 ** 31 - 65, 2 ** 31 - 65, vjp)  # the ends of the copies' coordinates
+        assert not on(bf16, 1, 1, 8, 1, 1000, 2 ** 31 - 64, vjp) and not on(bf16, 1, 1, 8, 1, 2 ** 31 - 64, 1000, vjp)
+        for bad in ((4, 3, 64), (4, 4, 60), (4, 4, 136)):
+            with pytest.raises(ValueError):
+                on(bf16, *bad, 2, 600, 600, vjp)
+    assert on(bf16, 65, 1, 64, 1, 600, 600) and not on(bf16, 65, 1, 64, 1, 600, 600, True)   # 65 heads to a key head
+    with pytest.raises(TypeError):
+        on(torch.float64, 4, 4, 64, 2, 600, 600)
