@@ -298,16 +298,25 @@ static int parts(long long blocks, long long fill, long long per, int step) {
 
 // 16-bit rows go to the tcgen05 kernels from this many rows of an average
 // structure on (and 64 senders).  They hold 128 rows and pad the head to 64 or
-// 128 values, so wide heads gain first.  64 structures, 8 BF16 heads, capped and
-// biased, strips against tcgen05 in us:
-//   forward   D 128: 50 rows 37/39, 96 rows 66/49;  D 64: 96 rows 35/43, 192 rows 75/83,
-//             16 structures of 256 rows 35/29;  D 16: 256 rows 67/100, 16 of 512 72/69
-//   with gradient   D 128: 50 rows 172/145;  D 64: 64 rows 96/129, 80 rows 185/152;
-//             D 32: 256 rows 348/353
-static int tc_rows(int D, bool vjp) {
-  if (D > 64) return vjp ? 48 : 72;
-  if (D > 32) return vjp ? 72 : 128;
-  return 320;
+// 128 values, so wide heads gain first; strips fill the second tile of 130 to 200
+// rows better, but only where there are blocks for more than two waves (`many`; 24
+// structures of 160 rows of 64: 26/36, 16 of them 25/25).
+// B structures, 8 BF16 heads, capped and biased, strips against tcgen05 in us:
+//   forward, D 128: B 64: 64 rows 40/40, 72 rows 60/48;  B 16: 72 rows 23/19
+//     D 64: B 64: 128 rows 42/46, 160 rows 66/81, 192 rows 76/83, 200 rows 103/91, 300 rows 170/146;
+//           B 16: 128 rows 20/19, 192 rows 28/25;  B 4: 128 rows 24/19, 192 rows 21/19
+//     D 32: B 64: 256 rows 79/91, 448 rows 202/209, 512 rows 251/226;  B 16: 256 rows 31/27, 448 rows 69/60;
+//           B 4: 512 rows 39/22
+//     D 16: B 64: 512 rows 210/222, 640 rows 316/316, 768 rows 444/419;  B 16: 256 rows 27/27;  B 4: 512 rows 34/23
+//   gradient, D 128: B 64: 64 rows 130/106
+//     D 64: B 64: 64 rows 67/92, 72 rows 124/105, 192 rows 275/222
+//     D 32: B 64, no bias: 192 rows 137/144, 224 rows 196/157;  biased: 256 rows 279/237
+//     D 16: B 64: 256 rows 238/227, 320 rows 344/361, 384 rows 455/397
+static int tc_rows(int D, bool vjp, bool many) {
+  if (vjp) return D > 64 ? 48 : D > 32 ? 72 : D > 16 ? 224 : 384;
+  if (D > 64) return 72;
+  if (!many) return D > 32 ? 128 : 256;
+  return D > 32 ? 200 : D > 16 ? 448 : 640;
 }
 AttnPlan attn_plan(const fc_attn_desc* d, int B, int nr, int ns) {
   AttnPlan p;
@@ -316,11 +325,12 @@ AttnPlan attn_plan(const fc_attn_desc* d, int B, int nr, int ns) {
   const int step = d->dtype == FC_F32 && d->head_dim > 64 ? 32 : 64;
   // (rows and the end of a tensor copy's box past the last sender fit 31 bits)
   const bool can = d->dtype != FC_F32 && per_s >= 64 && rows <= INT32_MAX - 64 && ns <= INT32_MAX - 64;
-  p.tc = can && per_r >= tc_rows(d->head_dim, false);
-  p.tc_vjp = can && per_r >= tc_rows(d->head_dim, true) && G <= 64;
+  const auto tiles = [&](long long n, int tile) { return (n + tile - 1) / tile > B ? (n + tile - 1) / tile : B; };
+  const bool many = B * ((per_r + 127) / 128) * KV > 2 * sms;   // more than two waves of tiles of 128
+  p.tc = can && per_r >= tc_rows(d->head_dim, false, many);
+  p.tc_vjp = can && per_r >= tc_rows(d->head_dim, true, many) && G <= 64;
   // few: up to two 16-row tiles a structure
   p.few = !p.tc && per_r <= 32;
-  const auto tiles = [&](long long n, int tile) { return (n + tile - 1) / tile > B ? (n + tile - 1) / tile : B; };
   p.splits = p.tc    ? parts(tiles(rows, 128) * KV, sms, per_s, 64)
              : p.few ? parts(tiles(rows, 16) * KV, 4 * sms, per_s, 64)
                      : parts(tiles(rows, 64) * KV, 2 * sms, per_s, step);

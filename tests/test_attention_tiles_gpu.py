@@ -64,7 +64,7 @@ def test_a_gradient_does_not_depend_on_the_others_asked_for(fc, apart, bias):  #
 def test_score_factors_far_from_one_of_narrow_heads(fc, power, d):  # noqa: F811
     """Queries and keys times 2^power and scale times 4^-power are the same scores (exact in BF16), here at lengths at
     which narrow heads take the tcgen05 kernels: their polynomial has scale / cap in its coefficients."""
-    c = on_tcgen05(fc, Case([350], None, 2, 2, d, BF16, cap=3.0))
+    c = on_tcgen05(fc, Case([400], None, 2, 2, d, BF16, cap=3.0))
     c.qw *= 2.0 ** power
     c.kw[:, : c.kv] *= 2.0 ** power
     c.scale *= 4.0 ** -power
