@@ -63,7 +63,7 @@ struct SortGeom {
 };
 static SortGeom sort_geom(int n, int V, int C) {
   SortGeom g{n, V, 1024, 0, 1, 32};
-  while (g.span < 128 && (long long)n / (2 * g.span) * ((C + 127) / 128) >= 8 * 148) g.span *= 2;
+  while (g.span < 128 && (long long)n / (2 * g.span) * ((C + 127) / 128) >= 8 * device_sm_count()) g.span *= 2;
   const long long per = ((long long)n + 511) / 512;
   if (per > g.rows) g.rows = (int)((per + 255) / 256 * 256);
   g.chunks = (int)(((long long)n + g.rows - 1) / g.rows);
