@@ -534,7 +534,7 @@ static VjpLayout vjp_layout(const fc_attn_desc* d, int B, int nr, int ns) {
 }
 
 struct VjpWants {
-  bool q, kv, pos_r, pos_s, self;
+  bool kv, self;
   float *pos_recv_bar, *pos_send_bar, *slope_bar;
 };
 

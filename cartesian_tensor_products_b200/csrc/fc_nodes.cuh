@@ -117,7 +117,6 @@ __device__ __forceinline__ void store_pack(T* p, const float (&in)[W]) {
 }
 
 inline bool row_dtype(int dtype) { return dtype == FC_F32 || dtype == FC_BF16 || dtype == FC_F16; }
-inline size_t row_size(int dtype) { return dtype == FC_F32 ? 4 : 2; }
 inline size_t round16(size_t b) { return (b + 15) & ~(size_t)15; }
 
 }  // namespace fc
