@@ -10,7 +10,8 @@
 // senders are split over blocks, whose partial rows a second kernel joins.
 // Bound by the latency of its few tiles (128 molecules of 9 to 70 atoms, 8 FP32
 // heads of 16: 21 us) and, on long FP32 structures, by the three TF32 products of
-// mma.sync (2 of 1000 nodes, 8 heads of 128: 327 us, 25 TFLOP/s of 4 n^2 H D).
+// mma.sync (2 of 1000 nodes, 8 heads of 128, cap and bias: 335 us, 24 TFLOP/s of
+// 4 n^2 H D).
 #include <math.h>
 
 #include "fc_attention.cuh"

@@ -7,12 +7,14 @@
 // only when the reference is raised.  The two groups take the tiles in turn,
 // each with its own state and output columns; they are merged at the end.
 //
-// Bound by the score arithmetic: two special functions (exp, root) and some 20
-// FP32 operations a pair of nodes and head against 4 D tensor operations.  16,384
-// nodes, 8 BF16 heads of 64, cap and bias: 2.02 ms, 1.06e12 pairs/s, 272 TFLOP/s
-// (47 % of the special functions' rate, FP32 pipe 41 %, tensor core 15 %; the
-// bytes would take 10 us); 4096 such nodes 159 us.  The rest is latency: eight warps of rows are all
-// that their registers leave room for.
+// The score arithmetic takes the time: two special functions (exp, and the root
+// of a distance, formed again for every head) and some 20 FP32 operations a pair
+// of nodes and head against 4 D tensor operations.  16,384 nodes, 8 BF16 heads of
+// 64, cap and bias: 2.04 ms, 1.05e12 pairs/s, 270 TFLOP/s (47 % of the special
+// functions' rate, FP32 pipe 41 %, tensor core 15 %; the bytes would take 10 us);
+// 4096 such nodes 157 us.  No pipe is full: eight warps of rows are all that
+// their registers leave room for, two a scheduler, which cannot hide the latency
+// of the tensor-memory reads and of each other's chains.
 #include <cudaTypedefs.h>
 #include <math.h>
 

@@ -167,7 +167,7 @@ __device__ __forceinline__ float max_pairs(const float2 (&x)[N]) {
 
 // f tanh(mul s) / s for |mul s| <= 0.6, as a polynomial in s^2 with the powers of
 // mul in its coefficients (degree 4, least largest relative error, fitted to
-// tanh(x)/x: 7.3e-8).  The FP32 pipe is what the score arithmetic fills first, so
+// tanh(x)/x; 9.1e-8 with FP32 coefficients).  The FP32 pipe is what the score arithmetic fills first, so
 // the narrower range of strip_tanh's 0.8 is given for two operations less.
 constexpr float kAtTanhMax = 0.6f;
 struct TanhPoly {

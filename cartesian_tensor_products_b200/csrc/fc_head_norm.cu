@@ -1,7 +1,9 @@
 // RMS norm of query and key heads with the rotation by node positions, and
 // its VJP, one pass over the rows each.
 //
-// Bound by the rows read and written.  A group of 1 to 32 lanes takes every
+// Near the rows read and written: neither their bytes nor the instructions fill
+// the time (52 and 40 of 78 us in the first case below), a third of the warps
+// leave both waiting in turn.  A group of 1 to 32 lanes takes every
 // hs-th head of a node, so that a warp reads one stretch of a row and the node's
 // angles stay in registers over the group's heads (a block forms them once, in
 // shared memory; one group per node instead read 64-byte pieces of eight rows
@@ -11,10 +13,11 @@
 // exchange.  W is the widest vector that R is a multiple of (any R is valid:
 // odd ones take scalar units).  Angles are formed in FP64 and reduced to half
 // turns, since FP32 would lose the phase of positions far from the origin.
-// 65,536 nodes of 16 + 4 BF16 heads of 64: 336 MB in 75 us (4.5 TB/s; some 17
-// instructions a value, angles included, at a third of the warps); the VJP at
+// 65,536 nodes of 16 + 4 BF16 heads of 64: 336 MB in 78 us (4.3 TB/s; some 17
+// instructions a value, angles included); the VJP at
 // 32,769 nodes of 8 + 2 BF16 heads of 128: 252 MB in 100 us (its registers leave
-// two blocks per SM).
+// two blocks per SM, and at 128 a thread the 16-bit rows of whole vectors spill
+// some 390 bytes).
 #include <math.h>
 
 #include "fc_device.cuh"
@@ -33,7 +36,8 @@ struct HeadArgs {
 // cos and sin of t half turns.  The quarter turns are taken off in FP64 (adding
 // and subtracting 1.5 2^52 rounds to a whole number, whose low bits are the
 // quadrant), the rest |f| <= 1/4 goes through polynomials in f^2 of least
-// largest error (fitted to sin(pi f)/f, relative, 3.2e-9, and cos(pi f), 4.7e-11).
+// largest error, fitted to sin(pi f)/f (relative) and cos(pi f).  With their
+// coefficients rounded to FP32 they are 3.4e-8 and 6.7e-9 off.
 __device__ __forceinline__ float2 half_turns(double t) {
   constexpr double kRound = 6755399441055744.0;
   const double m = fma(t, 2.0, kRound);

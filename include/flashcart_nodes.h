@@ -17,7 +17,9 @@
  * type per call (FC_F32, FC_BF16, FC_F16).  Positions, weights (gamma),
  * slopes, log-sums and the gradients of all of these and of tables are FP32.
  * Sums, norms and softmax statistics are held in FP32 or FP64 whatever the
- * row type, and results are rounded once.
+ * row type, and results are rounded once.  Inside the attention's matrix
+ * products, weights and score gradients of 16-bit rows are 16-bit values (see
+ * there), and FP32 operands are two TF32 terms (2^-20 of a value).
  * Heads.  A head is head_dim contiguous values, head_dim a multiple of 8 from
  * 8 to 128.  Head h of node n starts at n * ld + h * head_dim; the row step
  * ld (in values, a multiple of 8, at least heads * head_dim) lets queries,
@@ -65,7 +67,7 @@ int fc_species_embed_vjp(int dtype, int n_nodes, int n_species, int lmax, int ch
                          size_t ws_bytes, fc_stream_t stream);
 
 /* Query and key heads of a row: heads 0 .. heads_q - 1 are queries, the
- * heads_k after them keys (either count may be 0, not both).  pairs: the
+ * heads_k after them keys (either count may be 0, not both; at most 1024).  pairs: the
  * number R of rotated pairs, 0 <= 2 R <= head_dim. */
 typedef struct {
   int dtype;
@@ -82,8 +84,13 @@ typedef struct {
  *   y_f     = u_f cos(theta_f) - u_{f+R} sin(theta_f)
  *   y_{f+R} = u_f sin(theta_f) + u_{f+R} cos(theta_f),  y_d = u_d for d >= 2 R
  * so that the product of a rotated query and key depends on the difference of
- * their positions only.  Angles are formed and reduced in FP64: positions far
- * from the origin lose nothing.
+ * their positions only.  That is invariance under translation, not under
+ * rotation: with fixed frequency vectors the result depends on how a structure
+ * is turned, unless the model averages over directions (the attention's bias by
+ * distance has no such direction).  Angles are formed and reduced in FP64:
+ * positions far from the origin lose nothing.  The mean square is formed in
+ * FP32: |x| up to 1e18 (above, it overflows and the head comes out 0) and, if
+ * eps is 0, from 1e-18 on.
  *   x [n_nodes] rows of (heads_q + heads_k) heads, step ldx; y likewise, step
  *   ldy; gamma_q, gamma_k [head_dim] (NULL: ones); pos [n_nodes][3] and freq
  *   [3][R] (needed if R > 0). */
@@ -142,7 +149,9 @@ typedef struct {
  *   log).  A receiver with no sender left gets a zero row and lse -infinity.
  *   out_f32 [n_recv][heads][head_dim] FP32, or NULL: the output before its
  *   rounding, which the VJP reads.  16-bit types then carry the weights
- *   through the value product as two 16-bit terms.
+ *   through the value product as two 16-bit terms; without it as one (half a
+ *   unit of 2^-8 or 2^-11 of each weight, averaged over the row), while their
+ *   sum stays FP32.
  * workspace: fc_node_attention_workspace_size() bytes (0: none needed),
  * 16-byte aligned, ws_bytes = its real size. */
 size_t fc_node_attention_workspace_size(const fc_attn_desc *desc, int n_struct, int n_recv, int n_send);
